@@ -373,6 +373,79 @@ int hca_dense_attn_window(const void* q, const void* cache, const int64_t* t, co
                           void* workspace, size_t ws_bytes, int dtype, int out_bf16,
                           csa_stream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * The paged key-value cache of the stack's full-attention layers (DeepSeek's "Compressed
+ * Attention" page, layer stack: some layers keep attention over every token).  Keys and values are
+ * separate, n_kv heads of d elements, and G = n_h / n_kv query heads share a key head.
+ *
+ * K, V   : pools of pages (dtype, same strides).  Row r (0 <= r < page) of page p and head h is
+ *          the d contiguous elements at p*pool_ld_page + r*pool_ld_row + h*pool_ld_head
+ *          (elements), so [page][row][head] and [page][head][row] pools both fit, and
+ *          one pool with K and V halves.  0 <= p < n_pages, any page size >= 1.
+ * table  : int32 [B, max_pages] (device).  Token j of sequence b, 0 <= j < cap =
+ *          max_pages * page, lies in page table[b][j / page], row j mod page.  An entry
+ *          outside [0, n_pages) means that there is no page: its tokens are never read
+ *          or written, and no query sees them.  Sequences may share pages that no call writes.
+ * t      : int64 [B, nq] (device): the cache position of each new token; t < 0 marks
+ *          padding.  Positions count cached tokens, so after paged_evict they go on
+ *          from the new length.
+ * Constraints: 1 <= d <= 256 (paged_attn), cap < 2^31 - 1024.  Rows that no visible token has may hold
+ * anything, NaN included.
+ * ------------------------------------------------------------------------------- */
+
+/* paged_append - writes the keys and values of new tokens into their pages: token i of sequence b
+ * goes to cache position t[b][i].  k, v: [B, nq, n_kv, d] (dtype), element (b, i, h, x) at
+ * b*ld_batch + i*ld_tok + h*ld_head + x (same strides).  Tokens with t < 0, t >= cap or no page
+ * are left out.  Positions of one sequence must differ, and pages written must belong to one
+ * sequence: which of two tokens at one place stays is not specified. */
+int paged_append(const void* k, const void* v, int64_t ld_batch, int64_t ld_tok, int64_t ld_head,
+                 void* K, void* V, int64_t pool_ld_page, int64_t pool_ld_row, int64_t pool_ld_head,
+                 int64_t n_pages, int page, const int32_t* table, int max_pages, const int64_t* t,
+                 int B, int nq, int n_kv, int d, int dtype, csa_stream_t stream);
+
+/* paged_attn - attention of nq query tokens of each sequence over its cached tokens:
+ *   out[b][i][x] = sum_j softmax_j(scale * q[b][i][x] . K_j[x / G]) V_j[x / G]
+ * over the visible tokens j of query (b, i) at position t: j <= t (and j < cap), and if n_win > 0
+ * also j > t - n_win (the window, the token itself included) or j < n_sink (the first
+ * tokens, which stay visible).  n_win = 0: no window, n_sink has no effect.  nq = 1 is a decode
+ * step; a prompt is a call with its tokens' positions, after paged_append.  scale <= 0
+ * selects 1/sqrt(d).
+ *
+ * q, out : [B, nq, n_h, d]; out is fp32, or bf16 when out_bf16 != 0 (dtype must be bf16)
+ * lse    : fp32 [B, nq, n_h] natural-log sum of exp(scaled logits), or NULL
+ * acc, acc_out : both NULL, or fp32 [B, n_kv, cap]: acc_out[b][h][j] = acc[b][h][j] + the
+ *          attention weight that token j got from all queries and query heads of key head h.  They may
+ *          be the same buffer; every element of acc_out is written.
+ * A query that sees nothing gets out = 0 and lse = -inf.
+ * workspace : >= paged_attn_workspace_size(...) bytes, 16-byte aligned; weights != 0 when acc is
+ *          given.  Its contents need not be set and mean nothing between calls.
+ * The lengths are read on the device: a captured call follows t and table. */
+size_t paged_attn_workspace_size(int B, int nq, int n_h, int n_kv, int d, int64_t cap, int weights);
+int paged_attn(const void* q, const void* K, const void* V, int64_t pool_ld_page, int64_t pool_ld_row,
+               int64_t pool_ld_head, int64_t n_pages, int page, const int32_t* table, int max_pages,
+               const int64_t* t, int B, int nq, int n_h, int n_kv, int d, int n_win, int n_sink, float scale,
+               void* out, float* lse, const float* acc, float* acc_out, void* workspace, size_t ws_bytes,
+               int dtype, int out_bf16, csa_stream_t stream);
+
+/* paged_evict - cuts a cache back to its heaviest tokens.  Of the n = min(lens[b], cap) cached
+ * tokens of (b, h), new_lens[b] = min(n, keep) stay: all of them if n <= keep, else the first n_sink, the last
+ * n_recent, and of the others those with the largest acc[b][h][j] (ties: the lower j; NaN
+ * counts as lowest).  In their order they become tokens 0, 1, ... of the pages of
+ * new_table (int32 [B, new_max_pages], new_max_pages * page >= keep), of the same pools.
+ *
+ * lens, new_lens : int64 [B] (device)      acc : fp32 [B, n_kv, cap]
+ * new_acc : fp32 [B, n_kv, new_max_pages * page]: the kept tokens' weights, then zeros
+ * idx_out : int32 [B, n_kv, keep]: the kept tokens' old positions in rising order, then -1
+ * The pages of new_table must not be among those of table, and lie in no two places of it;
+ * new_table, new_lens and new_acc are not table, lens and acc (CSA_ERR_ARG).  The old pages are only read, so
+ * they may be shared.  A kept token without a page is moved as zeros.
+ * n_sink + n_recent <= keep. */
+int paged_evict(void* K, void* V, int64_t pool_ld_page, int64_t pool_ld_row, int64_t pool_ld_head,
+                int64_t n_pages, int page, const int32_t* table, int max_pages, const int64_t* lens,
+                const float* acc, int B, int n_kv, int d, int keep, int n_sink, int n_recent,
+                const int32_t* new_table, int new_max_pages, int64_t* new_lens, float* new_acc,
+                int32_t* idx_out, int dtype, csa_stream_t stream);
+
 /* Device status of a workspace of csa_indexer_topk, csa_sparse_attn or hca_dense_attn:
  * synchronises `stream` and returns CSA_OK, or CSA_ERR_TIMEOUT if a tensor-core kernel
  * of an earlier call gave up a bounded wait (its outputs are then invalid).  The status

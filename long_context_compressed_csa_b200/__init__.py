@@ -32,4 +32,8 @@ from ._binding import (  # noqa: F401
     hca_dense_attn,
     library,
     library_path,
+    paged_append,
+    paged_attn,
+    paged_attn_workspace_size,
+    paged_evict,
 )

@@ -47,6 +47,13 @@ _SIGS = {
                                 vp, sz, i32, i32, vp], i32),
     "hca_dense_attn_window": ([vp, vp, vp, vp, i32, i32, i32, i32, i64, i32, i32, i64, f32, vp, vp, vp,
                                sz, i32, i32, vp], i32),
+    "paged_append": ([vp, vp, i64, i64, i64, vp, vp, i64, i64, i64, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                      vp], i32),
+    "paged_attn_workspace_size": ([i32, i32, i32, i32, i32, i64, i32], sz),
+    "paged_attn": ([vp, vp, vp, i64, i64, i64, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp,
+                    vp, vp, vp, sz, i32, i32, vp], i32),
+    "paged_evict": ([vp, vp, i64, i64, i64, i64, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp,
+                     vp, i32, vp], i32),
 }
 
 
@@ -354,3 +361,98 @@ def hca_dense_attn(q, cache, t, m_prime, out, workspace, lse=None, scale=0.0, st
         _ptr(q), _ptr(cache), _ptr(t), _ptr(win), B, nq, n_h, c, N_cap, m_prime, int(n_win), win.shape[1],
         float(scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _dtype(q), out_bf16,
         _stream(stream)))
+
+
+def _here(*ts):
+    """The paged calls launch on the current device; tensors of another one are refused."""
+    import torch
+    _cuda(*ts)
+    for t in ts:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError("all tensors must be on the current device (cuda:%d)" % torch.cuda.current_device())
+
+
+def _pool(K, V, table, B):
+    """Strides and sizes of the pools K, V [n_pages, page, n_kv, d] (any page, row and head
+    strides, so a permuted [n_pages, n_kv, page, d] pool too) and of the page table [B, max_pages]."""
+    import torch
+    assert K.dim() == 4 and V.shape == K.shape and V.stride() == K.stride() and V.dtype == K.dtype
+    assert K.stride(3) == 1 or K.shape[3] == 1
+    assert table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B and table.is_contiguous()
+    n_pages, page, n_kv, d = K.shape
+    return (K.stride(0), K.stride(1), K.stride(2), n_pages, page, _ptr(table), table.shape[1]), n_kv, d
+
+
+def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
+    """Write the keys and values k, v [B,nq,n_kv,d] (any strides, last dim contiguous) of new tokens
+    into the pools [n_pages,page,n_kv,d] at cache positions t int64 [B,nq] (< 0: padding), through
+    the page table int32 [B,max_pages]."""
+    import torch
+    _here(k, v, K_pages, V_pages, table, t)
+    B, nq = k.shape[:2]
+    pool, n_kv, d = _pool(K_pages, V_pages, table, B)
+    assert k.shape == (B, nq, n_kv, d) and v.shape == k.shape and v.stride() == k.stride()
+    assert k.dtype == v.dtype == K_pages.dtype and (k.stride(3) == 1 or d == 1)
+    assert t.dtype == torch.int64 and t.shape == (B, nq) and t.is_contiguous()
+    _check("paged_append", library().paged_append(
+        _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), _ptr(K_pages), _ptr(V_pages), *pool, _ptr(t), B, nq,
+        n_kv, d, _dtype(K_pages), _stream(stream)))
+
+
+def paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, weights=False) -> int:
+    """Bytes of workspace of paged_attn; cap = max_pages * page, weights: with acc."""
+    return int(library().paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, 1 if weights else 0))
+
+
+def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.0, n_win=0, n_sink=0, acc=None,
+               acc_out=None, stream=None):
+    """Attention of q [B,nq,n_h,d] at cache positions t int64 [B,nq] over the paged cache: every token
+    up to t, or with n_win >= 1 the last n_win of them and the first n_sink tokens.
+
+    acc fp32 [B,n_kv,cap]: acc_out (acc itself if None) = acc + the weight that each cached token
+    got, summed over the queries and the query heads of its key head."""
+    import torch
+    _here(q, K_pages, V_pages, table, t, out, workspace, lse, acc, acc_out)
+    B, nq, n_h, d = q.shape
+    pool, n_kv, dk = _pool(K_pages, V_pages, table, B)
+    assert dk == d and q.dtype == K_pages.dtype and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
+    assert t.dtype == torch.int64 and t.shape == (B, nq) and t.is_contiguous()
+    assert lse is None or (lse.shape == (B, nq, n_h) and lse.dtype == torch.float32 and lse.is_contiguous())
+    if acc is None:
+        assert acc_out is None
+    else:
+        acc_out = acc if acc_out is None else acc_out
+        for x in (acc, acc_out):
+            assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (
+                B, n_kv, table.shape[1] * K_pages.shape[1])
+    assert workspace.is_contiguous()
+    _dtype(out)
+    out_bf16 = 1 if out.dtype.itemsize == 2 else 0
+    _check("paged_attn", library().paged_attn(
+        _ptr(q), _ptr(K_pages), _ptr(V_pages), *pool, _ptr(t), B, nq, n_h, n_kv, d, int(n_win), int(n_sink),
+        float(scale), _ptr(out), _ptr(lse), _ptr(acc), _ptr(acc_out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _dtype(q), out_bf16, _stream(stream)))
+
+
+def paged_evict(K_pages, V_pages, table, lens, acc, keep, new_table, new_lens, new_acc, idx_out, n_sink=0, n_recent=0,
+                stream=None):
+    """Cut a paged cache of lens int64 [B] tokens back to min(lens, keep) a key head: the first n_sink, the
+    last n_recent and the heaviest of the others by acc fp32 [B,n_kv,cap], moved in their order to
+    the pages of new_table int32 [B,new_max_pages] (none of them in table).  Writes new_lens int64
+    [B], new_acc fp32 [B,n_kv,new_cap] and the old positions idx_out int32 [B,n_kv,keep] (-1 = none)."""
+    import torch
+    _here(K_pages, V_pages, table, lens, acc, new_table, new_lens, new_acc, idx_out)
+    B = table.shape[0]
+    pool, n_kv, d = _pool(K_pages, V_pages, table, B)
+    page = K_pages.shape[1]
+    assert new_table.dtype == torch.int32 and new_table.dim() == 2 and new_table.shape[0] == B
+    assert new_table.is_contiguous()
+    for x in (lens, new_lens):
+        assert x.dtype == torch.int64 and x.shape == (B,) and x.is_contiguous()
+    for x, tab in ((acc, table), (new_acc, new_table)):
+        assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, tab.shape[1] * page)
+    assert idx_out.dtype == torch.int32 and idx_out.shape == (B, n_kv, keep) and idx_out.is_contiguous()
+    _check("paged_evict", library().paged_evict(
+        _ptr(K_pages), _ptr(V_pages), *pool, _ptr(lens), _ptr(acc), B, n_kv, d, int(keep), int(n_sink),
+        int(n_recent), _ptr(new_table), new_table.shape[1], _ptr(new_lens), _ptr(new_acc), _ptr(idx_out),
+        _dtype(K_pages), _stream(stream)))

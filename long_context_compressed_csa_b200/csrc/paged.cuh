@@ -1,0 +1,282 @@
+// The paged key-value cache of the full-attention layers: arguments, visibility, and the
+// device-side schedule that the attention kernels share.
+#pragma once
+#include "common.cuh"
+
+namespace csa {
+
+constexpr int kPagedMaxD = 256;    // widest head the kernels hold on chip
+constexpr int kPagedMaxCtas = 512; // CTAs of one attention launch (the workspace has two slots for each)
+constexpr int kPagedUnit = 32;     // cached tokens of one unit of the schedule (decode kernels)
+
+// Pools of K and V rows: row (p, r, h) of d elements starts p * ld_page + r * ld_row + h * ld_head
+// elements after the base; K and V have the same strides.
+struct PagedPool {
+    int64_t ld_page, ld_row, ld_head;
+    int64_t n_pages;
+    int page;
+    const int32_t* table;  // [B][max_pages]
+    int max_pages;
+};
+
+// Element offset of cached token j of sequence b (head 0), or -1 when the table has no page
+// of the pool there.  0 <= j < max_pages * page.
+CSA_DEV int64_t paged_row(const PagedPool& pl, int b, int j)
+{
+    const int p = (int)((unsigned)j / (unsigned)pl.page);
+    const int64_t id = pl.table[(int64_t)b * pl.max_pages + p];
+    if ((uint64_t)id >= (uint64_t)pl.n_pages) return -1;
+    return id * pl.ld_page + (int64_t)(j - p * pl.page) * pl.ld_row;
+}
+
+struct PagedAttnArgs {
+    const void *q, *K, *V;
+    PagedPool pl;
+    const int64_t* t;      // [B][nq]
+    int B, nq, n_h, n_kv, d;
+    int G;                 // query heads per key head
+    int n_win, n_sink;     // n_win = 0: every token up to t
+    int cap;               // max_pages * page
+    float scale_log2;      // softmax scale * log2(e)
+    void* out;
+    int out_bf16;
+    float* lse;            // [B][nq][n_h] or null
+    // Packed rows of one (sequence, key head): row i * G + g is head g of query i.  They are
+    // cut into tiles of R rows; an entry e = b * n_tiles + tile and a key head make one item.
+    int R, n_tiles;
+    int unit;              // cached tokens of a schedule unit
+    int min_units;         // units a CTA takes at least
+    int grid;              // CTAs launched
+    // workspace
+    int4* desc;            // [grid]: the split item that begins in this CTA {entry, head, last CTA, -}, entry -1: none
+    float* part_o;         // [2 * grid][R][d] unnormalised partial outputs
+    float2* part_ml;       // [2 * grid][R] their (running maximum, sum), base 2
+    // accumulated weights: scaled base-2 logits [B][n_kv][cap][n_tiles * R] and the final
+    // base-2 log-sum-exp [B][n_kv][n_tiles * R], both in the workspace; null: none asked for
+    float* logits;
+    float* lse2;
+    const float* acc;
+    float* acc_out;
+};
+
+// Tokens [0, sink) and [lo, hi) are visible to query i of sequence b, sink <= lo <= hi (empty: hi = 0).
+struct RowBounds { int lo, hi, sink; };
+CSA_DEV RowBounds paged_bounds(const PagedAttnArgs& a, int b, int i)
+{
+    const int64_t t = a.t[(int64_t)b * a.nq + i];
+    RowBounds r;
+    r.hi = t < 0 ? 0 : (int)min(t + 1, (int64_t)a.cap);
+    r.lo = a.n_win > 0 ? (int)min(max(t - a.n_win + 1, (int64_t)0), (int64_t)r.hi) : 0;
+    r.sink = min(a.n_sink, r.lo);
+    return r;
+}
+CSA_DEV bool paged_visible(const RowBounds& r, int j) { return j < r.hi && (j >= r.lo || j < r.sink); }
+
+// What an entry reads: units [0, s1) and [w0, ...), n units in all.  Every row of the entry
+// sees all of [lo_max, hi_min).
+struct PagedEntry {
+    int b, tile;
+    int s1, w0, n;
+    int lo_max, hi_min;
+    CSA_DEV int first_token(int u, int unit) const { return (u < s1 ? u : u - s1 + w0) * unit; }
+};
+
+CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
+{
+    PagedEntry r;
+    r.b = e / a.n_tiles;
+    r.tile = e - r.b * a.n_tiles;
+    const int row0 = r.tile * a.R, row1 = min(row0 + a.R, a.nq * a.G) - 1;
+    const int i1 = row1 / a.G;
+    int lo_min = INT32_MAX, hi_max = 0, sink = 0;
+    r.lo_max = 0;
+    r.hi_min = INT32_MAX;
+    for (int i = row0 / a.G; i <= i1; ++i) {
+        const RowBounds w = paged_bounds(a, r.b, i);
+        r.lo_max = max(r.lo_max, w.lo);
+        r.hi_min = min(r.hi_min, w.hi);
+        if (w.hi > 0) {
+            lo_min = min(lo_min, w.lo);
+            hi_max = max(hi_max, w.hi);
+            sink = max(sink, w.sink);
+        }
+    }
+    r.w0 = hi_max > 0 ? lo_min / a.unit : 0;
+    r.s1 = (sink + a.unit - 1) / a.unit;
+    if (r.s1 >= r.w0) r.s1 = r.w0 = 0;  // the first tokens reach the window: one range from 0
+    // a row tile that sees nothing still takes one (masked) unit: its outputs are written there
+    r.n = max(1, r.s1 + (hi_max + a.unit - 1) / a.unit - r.w0);
+    return r;
+}
+
+// The schedule.  The units of all items, in the order (entry, key head, unit), are one list
+// that is cut into equal runs, one for each CTA, whatever the sequences' lengths: a ragged
+// batch and one long sequence both fill the GPU.  Only the first and the last item of a run
+// can be cut, so a CTA writes at most two partial results; paged_attn_combine joins them in
+// the order of the CTAs.  The lengths are read on the device, so a captured graph follows them.
+struct PagedCursor {
+    int64_t at, end;       // this CTA's run of the list
+    int64_t W;
+    int ctas;              // CTAs that have a run
+    int e, h, u;           // entry, key head and unit within the item of `at`
+    PagedEntry en;
+};
+
+// T threads call it together; sh has T / 32 + 2 elements.  False: this CTA has no run.
+template <int T>
+CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedCursor& c)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int NB = a.B * a.n_tiles;
+    int64_t sum = 0;
+    int n0 = 0;
+    for (int e = tid; e < NB; e += T) {
+        const int n = paged_entry(a, e).n;
+        if (e == tid) n0 = n;
+        sum += n;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sh[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) total += sh[w];
+    c.W = total * a.n_kv;
+    c.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, c.W / a.min_units));
+    if (cta >= c.ctas) return false;
+    c.at = cta * c.W / c.ctas;
+    c.end = (cta + 1) * c.W / c.ctas;
+    int64_t before = 0;
+    for (int base = 0;; base += T) {
+        const int e = base + tid;
+        const int n = base == 0 ? n0 : e < NB ? paged_entry(a, e).n : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) sh[warp] = inc;
+        if (tid == 0) sh[T / 32] = -1;
+        __syncthreads();
+        int64_t all = before;
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) {
+            if (w == warp) inc += all;
+            all += sh[w];
+        }
+        // inc: units (of one key head) up to and with entry e
+        if (n > 0 && (inc - n) * a.n_kv <= c.at && c.at < inc * a.n_kv) {
+            sh[T / 32] = e;
+            sh[T / 32 + 1] = inc - n;
+        }
+        __syncthreads();
+        if (sh[T / 32] >= 0) break;
+        before = all;
+    }
+    c.e = (int)sh[T / 32];
+    const int64_t off = c.at - sh[T / 32 + 1] * a.n_kv;
+    c.en = paged_entry(a, c.e);
+    c.h = (int)(off / c.en.n);
+    c.u = (int)(off - (int64_t)c.h * c.en.n);
+    __syncthreads();  // sh may be reused
+    return true;
+}
+
+// The part of the current item that this CTA has, and where its result goes.
+struct PagedSegment {
+    int u0, u1;
+    bool whole;
+    int slot;  // of a partial result
+};
+// Called by one thread when an item's first part is partial: the combine's description of it.
+CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c, int cta)
+{
+    PagedSegment s;
+    s.u0 = c.u;
+    s.u1 = (int)min((int64_t)c.en.n, c.u + (c.end - c.at));
+    s.whole = s.u0 == 0 && s.u1 == c.en.n;
+    s.slot = 2 * cta + (s.u0 == 0 ? 1 : 0);
+    if (!s.whole && s.u0 == 0 && threadIdx.x == 0) {
+        // the run that has the item's last unit: unit x lies in run ((x + 1) ctas - 1) / W
+        const int64_t last = c.at + c.en.n - 1;
+        a.desc[cta] = make_int4(c.e, c.h, (int)(((last + 1) * c.ctas - 1) / c.W), 0);
+    }
+    return s;
+}
+// On to the next item; false at the end of the run.
+CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegment& s)
+{
+    c.at += s.u1 - s.u0;
+    if (c.at >= c.end) return false;
+    c.u = 0;
+    if (++c.h == a.n_kv) {
+        c.h = 0;
+        c.en = paged_entry(a, ++c.e);
+    }
+    return true;
+}
+
+// out / lse element of packed row r of tile `tile`: index of the (query, head) pair, or -1.
+CSA_DEV int64_t paged_out_row(const PagedAttnArgs& a, int b, int tile, int h, int r)
+{
+    const int row = tile * a.R + r;
+    if (row >= a.nq * a.G) return -1;
+    const int i = row / a.G;
+    return ((int64_t)b * a.nq + i) * a.n_h + h * a.G + (row - i * a.G);
+}
+
+// Stores of one result: element `at` of out, and a row's log-sum-exp (natural for the caller,
+// base 2 for the accumulated weights) from its running maximum and sum.
+CSA_DEV void paged_store(const PagedAttnArgs& a, int64_t at, float v)
+{
+    if (a.out_bf16)
+        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(a.out)[at] = v;
+}
+CSA_DEV void paged_store_lse(const PagedAttnArgs& a, int64_t o, int b, int tile, int h, int r, float m, float l)
+{
+    const float z = l > 0.f ? m + log2f(l) : -INFINITY;
+    if (a.lse) a.lse[o] = z * 0.6931471805599453f;
+    if (a.lse2) a.lse2[((int64_t)b * a.n_kv + h) * (a.n_tiles * a.R) + tile * a.R + r] = z;
+}
+
+// The end of a segment: so [NW][R][ld] and sm_m, sm_l [NW][R] hold the warps' results.  Joins them
+// and writes the item's output, or a partial result for paged_attn_combine.  All T threads.
+template <int T, int NW, int R>
+CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, const PagedSegment& sg, const float* so,
+                                  int ld, const float* sm_m, const float* sm_l)
+{
+    for (int x = threadIdx.x; x < R * a.d; x += T) {
+        const int r = x / a.d, col = x - r * a.d;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w * R + r]);
+        float L = 0.f, v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float m = sm_m[w * R + r];
+            if (m == -INFINITY) continue;
+            const float f = exp2f(m - M);
+            L = fmaf(f, sm_l[w * R + r], L);
+            v = fmaf(f, so[(w * R + r) * ld + col], v);
+        }
+        if (sg.whole) {
+            const int64_t o = paged_out_row(a, c.en.b, c.en.tile, c.h, r);
+            if (o < 0) continue;
+            paged_store(a, o * a.d + col, L > 0.f ? v / L : 0.f);
+            if (col == 0) paged_store_lse(a, o, c.en.b, c.en.tile, c.h, r, M, L);
+        } else {
+            const int64_t at = (int64_t)sg.slot * R + r;
+            a.part_o[at * a.d + col] = v;
+            if (col == 0) a.part_ml[at] = make_float2(M, L);
+        }
+    }
+}
+
+int launch_paged_mma(const PagedAttnArgs& a, int dtype, cudaStream_t stream);
+
+}  // namespace csa
