@@ -7,7 +7,6 @@ namespace csa {
 
 constexpr int kPagedMaxD = 256;    // widest head the kernels hold on chip
 constexpr int kPagedMaxCtas = 512; // CTAs of one attention launch (the workspace has two slots for each)
-constexpr int kPagedUnit = 32;     // cached tokens of one unit of the schedule (decode kernels)
 
 // Pools of K and V rows: row (p, r, h) of d elements starts p * ld_page + r * ld_row + h * ld_head
 // elements after the base; K and V have the same strides.
@@ -51,8 +50,8 @@ struct PagedAttnArgs {
     int4* desc;            // [grid]: the split item that begins in this CTA {entry, head, last CTA, -}, entry -1: none
     float* part_o;         // [2 * grid][R][d] unnormalised partial outputs
     float2* part_ml;       // [2 * grid][R] their (running maximum, sum), base 2
-    // accumulated weights: scaled base-2 logits [B][n_kv][cap][n_tiles * R] and the final
-    // base-2 log-sum-exp [B][n_kv][n_tiles * R], both in the workspace; null: none asked for
+    // accumulated weights: scaled base-2 logits [B][n_kv][nq * G][cap] and the final base-2
+    // log-sum-exp [B][n_kv][nq * G], both in the workspace; null: none asked for
     float* logits;
     float* lse2;
     const float* acc;
@@ -72,15 +71,20 @@ CSA_DEV RowBounds paged_bounds(const PagedAttnArgs& a, int b, int i)
 }
 CSA_DEV bool paged_visible(const RowBounds& r, int j) { return j < r.hi && (j >= r.lo || j < r.sink); }
 
-// What an entry reads: units [0, s1) and [w0, ...), n units in all.  Every row of the entry
-// sees all of [lo_max, hi_min).
+// What an entry reads: units [0, s1) and [w0, ...), n units in all.  Every row of the entry sees all
+// of [lo_max, hi_min); none sees a token outside [0, sink) and [lo_min, hi_max).
 struct PagedEntry {
     int b, tile;
     int s1, w0, n;
     int lo_max, hi_min;
+    int lo_min, hi_max, sink;
     CSA_DEV int first_token(int u, int unit) const { return (u < s1 ? u : u - s1 + w0) * unit; }
+    CSA_DEV bool seen(int j) const { return j < hi_max && (j >= lo_min || j < sink); }
 };
 
+// COOP: the 32 lanes of a warp share the queries of the entry (a tile of many queries); else the
+// calling thread reads them all.
+template <bool COOP>
 CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
 {
     PagedEntry r;
@@ -88,25 +92,46 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
     r.tile = e - r.b * a.n_tiles;
     const int row0 = r.tile * a.R, row1 = min(row0 + a.R, a.nq * a.G) - 1;
     const int i1 = row1 / a.G;
-    int lo_min = INT32_MAX, hi_max = 0, sink = 0;
-    r.lo_max = 0;
+    r.lo_min = INT32_MAX;
+    r.hi_max = r.sink = r.lo_max = 0;
     r.hi_min = INT32_MAX;
-    for (int i = row0 / a.G; i <= i1; ++i) {
+    for (int i = row0 / a.G + (COOP ? (int)(threadIdx.x & 31) : 0); i <= i1; i += COOP ? 32 : 1) {
         const RowBounds w = paged_bounds(a, r.b, i);
         r.lo_max = max(r.lo_max, w.lo);
         r.hi_min = min(r.hi_min, w.hi);
         if (w.hi > 0) {
-            lo_min = min(lo_min, w.lo);
-            hi_max = max(hi_max, w.hi);
-            sink = max(sink, w.sink);
+            r.lo_min = min(r.lo_min, w.lo);
+            r.hi_max = max(r.hi_max, w.hi);
+            r.sink = max(r.sink, w.sink);
         }
     }
-    r.w0 = hi_max > 0 ? lo_min / a.unit : 0;
-    r.s1 = (sink + a.unit - 1) / a.unit;
+    if (COOP) {
+        r.lo_max = __reduce_max_sync(0xffffffffu, r.lo_max);
+        r.hi_min = __reduce_min_sync(0xffffffffu, r.hi_min);
+        r.lo_min = __reduce_min_sync(0xffffffffu, r.lo_min);
+        r.hi_max = __reduce_max_sync(0xffffffffu, r.hi_max);
+        r.sink = __reduce_max_sync(0xffffffffu, r.sink);
+    }
+    r.w0 = r.hi_max > 0 ? r.lo_min / a.unit : 0;
+    r.s1 = (r.sink + a.unit - 1) / a.unit;
     if (r.s1 >= r.w0) r.s1 = r.w0 = 0;  // the first tokens reach the window: one range from 0
     // a row tile that sees nothing still takes one (masked) unit: its outputs are written there
-    r.n = max(1, r.s1 + (hi_max + a.unit - 1) / a.unit - r.w0);
+    r.n = max(1, r.s1 + (r.hi_max + a.unit - 1) / a.unit - r.w0);
     return r;
+}
+
+// Units of entry e (0 past the last one).  All lanes of a warp call it, lane l with e = e0 + l.
+template <bool COOP>
+CSA_DEV int paged_units(const PagedAttnArgs& a, int e, int NB)
+{
+    if (!COOP) return e < NB ? paged_entry<false>(a, e).n : 0;
+    int n = 0;
+    const int lane = threadIdx.x & 31, e0 = e - lane;
+    for (int k = 0; k < 32 && e0 + k < NB; ++k) {
+        const int m = paged_entry<true>(a, e0 + k).n;
+        if (lane == k) n = m;
+    }
+    return n;
 }
 
 // The schedule.  The units of all items, in the order (entry, key head, unit), are one list
@@ -123,16 +148,16 @@ struct PagedCursor {
 };
 
 // T threads call it together; sh has T / 32 + 2 elements.  False: this CTA has no run.
-template <int T>
+template <int T, bool COOP>
 CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedCursor& c)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int NB = a.B * a.n_tiles;
     int64_t sum = 0;
     int n0 = 0;
-    for (int e = tid; e < NB; e += T) {
-        const int n = paged_entry(a, e).n;
-        if (e == tid) n0 = n;
+    for (int base = 0; base < NB; base += T) {
+        const int n = paged_units<COOP>(a, base + tid, NB);
+        if (base == 0) n0 = n;
         sum += n;
     }
 #pragma unroll
@@ -150,7 +175,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedC
     int64_t before = 0;
     for (int base = 0;; base += T) {
         const int e = base + tid;
-        const int n = base == 0 ? n0 : e < NB ? paged_entry(a, e).n : 0;
+        const int n = base == 0 ? n0 : paged_units<COOP>(a, e, NB);
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -178,7 +203,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedC
     }
     c.e = (int)sh[T / 32];
     const int64_t off = c.at - sh[T / 32 + 1] * a.n_kv;
-    c.en = paged_entry(a, c.e);
+    c.en = paged_entry<COOP>(a, c.e);
     c.h = (int)(off / c.en.n);
     c.u = (int)(off - (int64_t)c.h * c.en.n);
     __syncthreads();  // sh may be reused
@@ -207,6 +232,7 @@ CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c,
     return s;
 }
 // On to the next item; false at the end of the run.
+template <bool COOP>
 CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegment& s)
 {
     c.at += s.u1 - s.u0;
@@ -214,7 +240,7 @@ CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegme
     c.u = 0;
     if (++c.h == a.n_kv) {
         c.h = 0;
-        c.en = paged_entry(a, ++c.e);
+        c.en = paged_entry<COOP>(a, ++c.e);
     }
     return true;
 }
@@ -241,8 +267,11 @@ CSA_DEV void paged_store_lse(const PagedAttnArgs& a, int64_t o, int b, int tile,
 {
     const float z = l > 0.f ? m + log2f(l) : -INFINITY;
     if (a.lse) a.lse[o] = z * 0.6931471805599453f;
-    if (a.lse2) a.lse2[((int64_t)b * a.n_kv + h) * (a.n_tiles * a.R) + tile * a.R + r] = z;
+    if (a.lse2) a.lse2[((int64_t)b * a.n_kv + h) * (a.nq * a.G) + tile * a.R + r] = z;
 }
+
+// Rows of tile `tile` that are rows of the call.
+CSA_DEV int paged_rows(const PagedAttnArgs& a, int tile) { return min(a.R, a.nq * a.G - tile * a.R); }
 
 // The end of a segment: so [NW][R][ld] and sm_m, sm_l [NW][R] hold the warps' results.  Joins them
 // and writes the item's output, or a partial result for paged_attn_combine.  All T threads.
@@ -250,7 +279,8 @@ template <int T, int NW, int R>
 CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, const PagedSegment& sg, const float* so,
                                   int ld, const float* sm_m, const float* sm_l)
 {
-    for (int x = threadIdx.x; x < R * a.d; x += T) {
+    const int n = paged_rows(a, c.en.tile) * a.d;
+    for (int x = threadIdx.x; x < n; x += T) {
         const int r = x / a.d, col = x - r * a.d;
         float M = -INFINITY;
 #pragma unroll
@@ -266,7 +296,6 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
         }
         if (sg.whole) {
             const int64_t o = paged_out_row(a, c.en.b, c.en.tile, c.h, r);
-            if (o < 0) continue;
             paged_store(a, o * a.d + col, L > 0.f ? v / L : 0.f);
             if (col == 0) paged_store_lse(a, o, c.en.b, c.en.tile, c.h, r, M, L);
         } else {
@@ -277,6 +306,15 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
     }
 }
 
-int launch_paged_mma(const PagedAttnArgs& a, int dtype, cudaStream_t stream);
+// Which kernel a call runs on, its row tile, and the units and CTAs of its schedule.
+enum PagedKind { kPagedSimt, kPagedMma, kPagedF32 };
+struct PagedShape {
+    PagedKind kind;
+    int DP;         // head width rounded up to a kernel's
+    int WR;         // kPagedMma: row groups of 16; kPagedF32: rows
+    int R, unit, min_units, grid;
+};
+PagedShape paged_decode_shape(int dtype, int rows, int d);
+int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream);
 
 }  // namespace csa

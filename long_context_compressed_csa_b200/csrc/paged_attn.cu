@@ -18,6 +18,7 @@ namespace {
 constexpr int kSimtThreads = 128;
 constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtRows = 8;
+constexpr int kSimtUnit = 32;  // cached tokens of a schedule unit: one for each lane
 
 // The plain kernel.  A warp takes a unit of 32 cached tokens: lane = token for the logits, lane =
 // column for the products with V.  Element-wise loads, so every layout is right; the tensor-core
@@ -25,7 +26,7 @@ constexpr int kSimtRows = 8;
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 {
-    constexpr int R = kSimtRows, U = kPagedUnit, NC = kPagedMaxD / 32;
+    constexpr int R = kSimtRows, U = kSimtUnit, NC = kPagedMaxD / 32;
     extern __shared__ float smem[];
     __shared__ int64_t sh[kSimtThreads / 32 + 2];
     __shared__ float sm_m[kSimtWarps][R], sm_l[kSimtWarps][R];
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     PagedCursor c;
-    if (!paged_schedule<kSimtThreads>(a, cta, sh, c)) return;
+    if (!paged_schedule<kSimtThreads, false>(a, cta, sh, c)) return;
     const T* K = static_cast<const T*>(a.K);
     const T* V = static_cast<const T*>(a.V);
     while (true) {
@@ -79,8 +80,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
                                  paged_visible(paged_bounds(a, en.b, row / a.G), j);
                 any |= vis;
                 s[r] = vis ? s[r] * a.scale_log2 : -INFINITY;
-                if (a.logits && j < a.cap)
-                    a.logits[(((int64_t)en.b * a.n_kv + c.h) * a.cap + j) * (a.n_tiles * R) + row] = s[r];
+                if (a.logits && j < a.cap && row < a.nq * a.G)
+                    a.logits[(((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap + j] = s[r];
                 float top = s[r];
 #pragma unroll
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
         __syncthreads();
         paged_finish_segment<kSimtThreads, kSimtWarps, R>(a, c, sg, so, d, &sm_m[0][0], &sm_l[0][0]);
         __syncthreads();
-        if (!paged_next(a, c, sg)) break;
+        if (!paged_next<false>(a, c, sg)) break;
     }
 }
 
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
     const int j = blockIdx.x * kWeightThreads + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
     if (j >= a.cap) return;
     const int64_t g = (int64_t)b * a.n_kv + h, at = g * a.cap + j;
-    const int rows = a.n_tiles * a.R;
-    const float* s = a.logits + at * rows;
+    const int rows = a.nq * a.G;
+    const float* s = a.logits + g * rows * a.cap + j;
     const float* z = a.lse2 + g * rows;
     float w = 0.f;
     for (int i = 0; i < a.nq; ++i) {
@@ -213,7 +214,8 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
         for (int r = i * a.G; r < (i + 1) * a.G; ++r) {
             // every visible logit was written; -inf (a token without a page) weighs nothing,
             // and with no visible row at all lse is -inf too
-            if (s[r] != -INFINITY) w += exp2f(s[r] - z[r]);
+            const float x = s[(int64_t)r * a.cap];
+            if (x != -INFINITY) w += exp2f(x - z[r]);
         }
     }
     a.acc_out[at] = a.acc[at] + w;
@@ -221,28 +223,40 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
 
 }  // namespace
 
-// CTAs, rows per tile and workspace layout of a call, from its sizes alone (host arithmetic).
+// The kernel of a call.  The CUDA-core kernel takes what the others cannot load 16 bytes at a time.
+static PagedShape paged_shape(int dtype, bool wide, int rows, int d)
+{
+    if (wide) return paged_decode_shape(dtype, rows, d);
+    PagedShape s{};
+    s.kind = kPagedSimt;
+    s.R = kSimtRows;
+    s.unit = kSimtUnit;
+    s.min_units = kSimtWarps;
+    s.grid = 2 * kNumSMs;
+    return s;
+}
+
+// Workspace layout, from the sizes alone: room for every kernel that a call of these sizes may run on.
 struct PagedPlan {
-    int R, n_tiles, grid, unit, min_units;
-    size_t part_o, part_ml, logits, lse2, bytes;  // offsets after the 256-byte status block and desc
+    size_t part_o, part_ml, logits, lse2, bytes;  // offsets; before them the 256-byte status block and desc
 };
 
 static PagedPlan paged_plan(int B, int nq, int G, int n_kv, int d, int64_t cap, bool weights)
 {
     PagedPlan p{};
-    p.R = kSimtRows;
-    p.unit = kPagedUnit;
-    p.min_units = kSimtWarps;
-    p.n_tiles = (int)(((int64_t)nq * G + p.R - 1) / p.R);
-    const int64_t units = (cap + p.unit - 1) / p.unit * B * n_kv * p.n_tiles;
-    p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kNumSMs, units));
+    size_t slots = 0;  // rows of partial results
+    for (int dtype : {CSA_BF16, CSA_F32})
+        for (bool wide : {false, true}) {
+            const PagedShape s = paged_shape(dtype, wide, nq * G, d);
+            slots = std::max(slots, (size_t)2 * s.grid * s.R);
+        }
     size_t at = 256 + align_up(sizeof(int4) * kPagedMaxCtas, 256);
     p.part_ml = at;
-    at += align_up((size_t)2 * p.grid * p.R * sizeof(float2), 256);
+    at += align_up(slots * sizeof(float2), 256);
     p.part_o = at;
-    at += align_up((size_t)2 * p.grid * p.R * d * sizeof(float), 256);
+    at += align_up(slots * d * sizeof(float), 256);
     if (weights) {
-        const size_t rows = (size_t)B * n_kv * p.n_tiles * p.R;
+        const size_t rows = (size_t)B * n_kv * nq * G;
         p.lse2 = at;
         at += align_up(rows * sizeof(float), 256);
         p.logits = at;
@@ -286,17 +300,26 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     if ((((uintptr_t)q | (uintptr_t)K | (uintptr_t)V) & eb) || ((uintptr_t)out & (out_bf16 ? 1 : 3)) ||
         (((uintptr_t)lse | (uintptr_t)acc | (uintptr_t)acc_out | (uintptr_t)table) & 3) || ((uintptr_t)t & 7))
         return CSA_ERR_ALIGN;
-    const PagedPlan p = paged_plan(B, nq, n_h / n_kv, n_kv, d, cap, acc != nullptr);
+    const int G = n_h / n_kv;
+    const PagedPlan p = paged_plan(B, nq, G, n_kv, d, cap, acc != nullptr);
     if (!workspace || ws_bytes < p.bytes) return CSA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return CSA_ERR_ALIGN;
 
     PagedAttnArgs a{};
     a.q = q; a.K = K; a.V = V; a.pl = pl; a.t = t;
-    a.B = B; a.nq = nq; a.n_h = n_h; a.n_kv = n_kv; a.d = d; a.G = n_h / n_kv;
+    a.B = B; a.nq = nq; a.n_h = n_h; a.n_kv = n_kv; a.d = d; a.G = G;
     a.n_win = n_win; a.n_sink = n_win > 0 ? n_sink : 0; a.cap = (int)cap;
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * kLog2e;
     a.out = out; a.out_bf16 = out_bf16; a.lse = lse;
-    a.R = p.R; a.n_tiles = p.n_tiles; a.unit = p.unit; a.min_units = p.min_units; a.grid = p.grid;
+    // 16-byte loads: every row starts on a 16-byte boundary and is whole 16-byte words
+    const int64_t lds = pool_ld_page | pool_ld_row | (n_kv > 1 ? pool_ld_head : 0) | d;
+    const bool wide = aligned16(q) && aligned16(K) && aligned16(V) && lds * elem_bytes(dtype) % 16 == 0;
+    const PagedShape sp = paged_shape(dtype, wide, nq * G, d);
+    a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units;
+    a.n_tiles = (nq * G + sp.R - 1) / sp.R;
+    // no more CTAs than the capacity has units
+    const int64_t units = std::max<int64_t>(1, (cap + sp.unit - 1) / sp.unit) * B * n_kv * a.n_tiles;
+    a.grid = (int)std::max<int64_t>(1, std::min<int64_t>(sp.grid, units / sp.min_units));
     char* ws = static_cast<char*>(workspace);
     a.desc = reinterpret_cast<int4*>(ws + 256);
     a.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);
@@ -308,15 +331,19 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
         a.acc_out = acc_out;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t smem = ((size_t)a.R * d + std::max<size_t>((size_t)kSimtWarps * a.R * d, kSimtWarps * kPagedUnit * a.R)) *
-                        sizeof(float);
-    if (dtype == CSA_BF16)
-        launch_pdl(paged_attn_simt<__nv_bfloat16>, dim3(p.grid), dim3(kSimtThreads), smem, s, a);
-    else
-        launch_pdl(paged_attn_simt<float>, dim3(p.grid), dim3(kSimtThreads), smem, s, a);
-    st = launch_status();
+    if (sp.kind == kPagedSimt) {
+        const size_t smem =
+            ((size_t)a.R * d + std::max<size_t>((size_t)kSimtWarps * a.R * d, kSimtWarps * kSimtUnit * a.R)) * sizeof(float);
+        if (dtype == CSA_BF16)
+            launch_pdl(paged_attn_simt<__nv_bfloat16>, dim3(a.grid), dim3(kSimtThreads), smem, s, a);
+        else
+            launch_pdl(paged_attn_simt<float>, dim3(a.grid), dim3(kSimtThreads), smem, s, a);
+        st = launch_status();
+    } else {
+        st = launch_paged_decode(a, sp, s);
+    }
     if (st != CSA_OK) return st;
-    launch_pdl(paged_attn_combine, dim3(p.grid, p.R), dim3(kJoinThreads), 0, s, a);
+    launch_pdl(paged_attn_combine, dim3(a.grid, std::min(a.R, nq * G)), dim3(kJoinThreads), 0, s, a);
     st = launch_status();
     if (st != CSA_OK || !acc || cap == 0) return st;
     launch_pdl(paged_weights_kernel, dim3((unsigned)((cap + kWeightThreads - 1) / kWeightThreads), n_kv, B),

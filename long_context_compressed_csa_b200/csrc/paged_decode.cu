@@ -1,0 +1,582 @@
+// paged_attn for few query rows: the decode kernels, bound by the bytes of the cache.
+//
+// A CTA has kWarps warps in token groups.  A group owns every kWarps / WR-th unit (a few cached
+// tokens) of the CTA's run and a ring of stages that its lanes fill with 16-byte cp.async, two
+// units ahead of the one being used; a token that no row sees, or without a page, is zero-filled and
+// not read.  Each group keeps its own running maximum, sum and output, so groups never wait for
+// one another inside a run; they are joined once at its end.
+//   bf16: the rows are the 16-row operand of mma.sync (m16n8k16), K is its B operand as stored,
+//         V through transposing ldmatrix.  The weights go to the second product as two bf16
+//         parts (hi + lo), which keeps 16 bits of them at the price of tensor work that is idle anyway.
+//         WR > 1: WR warps of a group have 16 rows each and share the group's ring.
+//   fp32: plain FMAs, a token spread over LT lanes, RT rows in registers.
+#include "cluster.cuh"
+#include "paged.cuh"
+#include "tc_utils.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+
+CSA_DEV void cp16(uint32_t dst, const void* src, bool take)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+CSA_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+CSA_DEV void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+CSA_DEV void ldsm4(uint32_t (&r)[4], uint32_t p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(p));
+}
+CSA_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(p));
+}
+CSA_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+CSA_DEV uint32_t pack2(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+CSA_DEV float lo16(uint32_t u) { return __uint_as_float(u << 16); }
+CSA_DEV float hi16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Byte offset of 16-byte chunk c of row r of a stage's K or V block; the XOR spreads the 8 rows
+// that an ldmatrix (or the lanes of an fp32 load) touches over the banks.
+template <int ROWB>
+CSA_DEV uint32_t at16(int r, int c) { return r * ROWB + ((c ^ (r & 7)) << 4); }
+
+template <int WR>
+CSA_DEV void group_sync(int group)
+{
+    if (WR == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * WR) : "memory");
+}
+
+// The filling side of a group's ring: ROWB bytes a row, U rows of K and of V a stage.
+template <int ROWB, int U, int WR>
+struct Ring {
+    static constexpr int kChunks = ROWB / 16, kLanes = 32 * WR;
+    static constexpr int kStage = 2 * U * ROWB;
+    uint32_t base;          // shared address of the group's ring
+    uint32_t* masks;        // [stages]: bit r of a word: row r has a token
+    const char *K, *V;      // of this key head
+    int row_bytes;          // d elements
+    int lane;               // within the group
+
+    // Start of the loads of unit u into `stage`; every lane of the group.
+    CSA_DEV void load(const PagedAttnArgs& a, const PagedEntry& en, int u, int stage, int eb)
+    {
+        const int j0 = en.first_token(u, U), l = lane & 31;
+        int64_t off = -1;
+        if (l < U && j0 + l < a.cap && en.seen(j0 + l)) off = paged_row(a.pl, en.b, j0 + l);
+        const unsigned have = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) masks[stage] = have;
+        off *= eb;
+        const uint32_t s = base + stage * kStage;
+        // a pass takes kLanes chunks: kLanes / kChunks rows, or a part of one row
+        constexpr int kPasses = U * kChunks / kLanes;
+        static_assert(U * kChunks % kLanes == 0, "whole passes");
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int x = i * kLanes + lane, r = x / kChunks, c = x % kChunks;
+            const int64_t o = __shfl_sync(0xffffffffu, off, r);
+            const bool take = o >= 0 && c * 16 < row_bytes;
+            const int64_t at = take ? o + c * 16 : 0;
+            cp16(s + at16<ROWB>(r, c), K + at, take);
+            cp16(s + U * ROWB + at16<ROWB>(r, c), V + at, take);
+        }
+    }
+};
+
+template <int DP, int WR>
+struct MmaShape {
+    static constexpr int kWT = kWarps / WR;                        // token groups
+    static constexpr int kU = DP == 64 || (WR > 1 && DP == 128) ? 32 : 16;
+    static constexpr int kStages = WR == 4 ? 6 : 3;
+    static constexpr int kRows = 16 * WR;
+    static constexpr int kRing = kWT * kStages * 2 * kU * DP * 2;  // bytes
+    static constexpr int kQ = DP == 256 ? kRows * DP * 2 : 0;      // wide heads: q in shared memory
+    static constexpr int kJoin = kWT * kRows * (DP + 8) * 4;       // over the ring at a segment's end
+    static constexpr int kSmem = kQ + (kRing > kJoin ? kRing : kJoin);
+    static constexpr int kCtas = kSmem <= 112 * 1024 ? 2 : 1;      // on an SM
+};
+
+template <int DP, int WR>
+__global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_mma(PagedAttnArgs a)
+{
+    using S = MmaShape<DP, WR>;
+    constexpr int U = S::kU, R = S::kRows, WT = S::kWT, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t sh[kWarps + 2];
+    __shared__ float sm_m[WT * R], sm_l[WT * R];
+    __shared__ uint32_t masks[WT * NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    const int group = warp / WR, wr = warp % WR;
+    uint8_t* sring = smem + S::kQ;
+    float* so = reinterpret_cast<float*>(sring);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    PagedCursor c;
+    if (!paged_schedule<kThreads, false>(a, cta, sh, c)) return;
+    Ring<ROWB, U, WR> ring;
+    ring.base = tc::smem_u32(sring) + group * (NS * ring.kStage);
+    ring.masks = masks + group * NS;
+    ring.row_bytes = a.d * 2;
+    ring.lane = wr * 32 + lane;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    const uint32_t sq = tc::smem_u32(smem) + wr * 16 * ROWB;
+    const int r0 = wr * 16 + (lane >> 2);  // this lane's rows: r0 and r0 + 8
+    while (true) {
+        const PagedSegment sg = paged_segment(a, c, cta);
+        const PagedEntry en = c.en;
+        ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
+        ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
+        const int first = sg.u0 + group, n_u = first < sg.u1 ? (sg.u1 - first + WT - 1) / WT : 0;
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) {
+            if (s < n_u) ring.load(a, en, first + s * WT, s, 2);
+            cp_commit();
+        }
+        uint32_t qf[DP == 256 ? 1 : KS][4];
+        if constexpr (DP == 256) {
+            for (int x = tid; x < R * (DP / 8); x += kThreads) {
+                const int r = x / (DP / 8), ch = x % (DP / 8);
+                const int64_t o = paged_out_row(a, en.b, en.tile, c.h, r);
+                const bool in = o >= 0 && ch * 8 < a.d;
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(q + o * a.d + ch * 8) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(smem + at16<ROWB>(r, ch)) = v;
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int64_t o = paged_out_row(a, en.b, en.tile, c.h, r0 + 8 * half);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int col = k * 16 + p * 8 + 2 * (lane & 3);
+                        qf[k][2 * p + half] =
+                            o >= 0 && col < a.d ? *reinterpret_cast<const uint32_t*>(q + o * a.d + col) : 0u;
+                    }
+            }
+        }
+        RowBounds rb[2];
+        bool row_in[2];
+        float* lg[2];  // the rows' logits, when they are asked for
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = en.tile * R + r0 + 8 * half;
+            row_in[half] = row < a.nq * a.G;
+            rb[half] = row_in[half] ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
+            lg[half] = a.logits && row_in[half]
+                           ? a.logits + (((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap
+                           : nullptr;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[DP / 8][4];
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+        int st = 0;
+        for (int i = 0; i < n_u; ++i) {
+            cp_wait<NS - 2>();
+            group_sync<WR>(group);
+            const int u = first + i * WT;
+            {
+                const int nx = st == 0 ? NS - 1 : st - 1;
+                if (i + NS - 1 < n_u) ring.load(a, en, u + (NS - 1) * WT, nx, 2);
+                cp_commit();
+            }
+            const uint32_t sk = ring.base + st * ring.kStage, sv = sk + U * ROWB;
+            const unsigned have = ring.masks[st];
+            st = st == NS - 1 ? 0 : st + 1;
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[t][x] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t qk[4];
+                if constexpr (DP == 256)
+                    ldsm4(qk, sq + at16<ROWB>((lane & 7) + (lane & 8), 2 * k + (lane >> 4)));
+                else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) qk[x] = qf[k][x];
+                }
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) {
+                    uint32_t b[4];  // tokens t*8 .. +15, k16 step k: {n0 k0, n0 k8, n8 k0, n8 k8}
+                    ldsm4(b, sk + at16<ROWB>(t * 8 + (lane & 7) + ((lane & 16) >> 1), 2 * k + ((lane >> 3) & 1)));
+                    mma16816(s[t], qk, b[0], b[1]);
+                    mma16816(s[t + 1], qk, b[2], b[3]);
+                }
+            }
+            const int j0 = en.first_token(u, U);
+            const bool clear = j0 >= en.lo_max && j0 + U <= en.hi_min && have == (U == 32 ? ~0u : (1u << (U & 31)) - 1);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int r = t * 8 + 2 * (lane & 3) + (x & 1);
+                    float v = s[t][x] * a.scale_log2;
+                    if (!clear && !((have >> r & 1) && paged_visible(rb[x >> 1], j0 + r))) v = -INFINITY;
+                    s[t][x] = v;
+                    top[x >> 1] = fmaxf(top[x >> 1], v);
+                }
+                if (a.logits) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int j = j0 + t * 8 + 2 * (lane & 3) + (x & 1);
+                        if (lg[x >> 1] && j < a.cap) lg[x >> 1][j] = s[t][x];
+                    }
+                }
+            }
+            float shrink[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+                const float mn = fmaxf(m[half], top[half]);
+                shrink[half] = mn == m[half] ? 1.f : exp2f(m[half] - mn);  // m = -inf: 0
+                m[half] = mn;
+                l[half] *= shrink[half];
+            }
+            if (__any_sync(0xffffffffu, shrink[0] != 1.f || shrink[1] != 1.f)) {
+#pragma unroll
+                for (int i2 = 0; i2 < DP / 8; ++i2)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[i2][x] *= shrink[x >> 1];
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[t][x] = tc::ex2_approx(s[t][x] - base[x >> 1]);
+                    l[x >> 1] += s[t][x];
+                }
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float p = s[t + (x >> 1)][2 * (x & 1)], p1 = s[t + (x >> 1)][2 * (x & 1) + 1];
+                    hi[x] = pack2(p, p1);
+                    lo[x] = pack2(p - lo16(hi[x]), p1 - hi16(hi[x]));
+                }
+#pragma unroll
+                for (int n = 0; n < DP / 8; n += 2) {
+                    uint32_t b[4];  // tokens t*8 .. +15, columns n*8 .. +15: {k0 n0, k8 n0, k0 n8, k8 n8}
+                    ldsm4_t(b, sv + at16<ROWB>(t * 8 + (lane & 15), n + (lane >> 4)));
+                    mma16816(o[n], hi, b[0], b[1]);
+                    mma16816(o[n + 1], hi, b[2], b[3]);
+                    mma16816(o[n], lo, b[0], b[1]);
+                    mma16816(o[n + 1], lo, b[2], b[3]);
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();  // every group is done with its ring: so lies over it
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+            if ((lane & 3) == 0) {
+                sm_m[group * R + r0 + 8 * half] = m[half];
+                sm_l[group * R + r0 + 8 * half] = l[half];
+            }
+            if (row_in[half]) {
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n)
+                    *reinterpret_cast<float2*>(so + (group * R + r0 + 8 * half) * (DP + 8) + n * 8 + 2 * (lane & 3)) =
+                        make_float2(o[n][2 * half], o[n][2 * half + 1]);
+            }
+        }
+        __syncthreads();
+        paged_finish_segment<kThreads, WT, R>(a, c, sg, so, DP + 8, sm_m, sm_l);
+        __syncthreads();
+        if (!paged_next<false>(a, c, sg)) break;
+    }
+}
+
+template <int DP, int RT>
+struct F32Shape {
+    static constexpr int kEL = 64 / RT;      // elements of a row that a lane has
+    static constexpr int kLT = DP / kEL;     // lanes of a token
+    static constexpr int kNG = 32 / kLT;     // tokens at a time
+    static constexpr int kU = 1024 / DP;     // tokens of a unit: 8 KB of K and V
+    static constexpr int kStages = 3;
+    static constexpr int kRing = kWarps * kStages * 2 * kU * DP * 4;
+    static constexpr int kJoin = kWarps * RT * (DP + 4) * 4;
+    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int DP, int RT>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
+{
+    using S = F32Shape<DP, RT>;
+    constexpr int U = S::kU, NS = S::kStages, EL = S::kEL, LT = S::kLT, NG = S::kNG, TG = U / NG, ROWB = DP * 4;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t sh[kWarps + 2];
+    __shared__ float sm_m[kWarps * RT], sm_l[kWarps * RT];
+    __shared__ uint32_t masks[kWarps * NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    const int g = lane / LT, e = lane % LT;
+    float* so = reinterpret_cast<float*>(smem);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    PagedCursor c;
+    if (!paged_schedule<kThreads, false>(a, cta, sh, c)) return;
+    Ring<ROWB, U, 1> ring;
+    ring.base = tc::smem_u32(smem) + warp * (NS * ring.kStage);
+    ring.masks = masks + warp * NS;
+    ring.row_bytes = a.d * 4;
+    ring.lane = lane;
+    const uint8_t* my = smem + warp * (NS * ring.kStage);
+    const float* q = static_cast<const float*>(a.q);
+    while (true) {
+        const PagedSegment sg = paged_segment(a, c, cta);
+        const PagedEntry en = c.en;
+        ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 4;
+        ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 4;
+        const int first = sg.u0 + warp, n_u = first < sg.u1 ? (sg.u1 - first + kWarps - 1) / kWarps : 0;
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) {
+            if (s < n_u) ring.load(a, en, first + s * kWarps, s, 4);
+            cp_commit();
+        }
+        float2 qr[RT][EL / 2], o[RT][EL / 2];
+        float m[RT], l[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int64_t at = paged_out_row(a, en.b, en.tile, c.h, r);
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int x = 0; x < EL / 2; ++x) {
+                const int col = (e + LT * (x / 2)) * 4 + 2 * (x & 1);
+                qr[r][x] = o[r][x] = make_float2(0.f, 0.f);
+                if (at >= 0 && col < a.d) {
+                    qr[r][x].x = q[at * a.d + col];
+                    if (col + 1 < a.d) qr[r][x].y = q[at * a.d + col + 1];
+                }
+            }
+        }
+        int st = 0;
+        for (int i = 0; i < n_u; ++i) {
+            cp_wait<NS - 2>();
+            __syncwarp();
+            const int u = first + i * kWarps;
+            {
+                const int nx = st == 0 ? NS - 1 : st - 1;
+                if (i + NS - 1 < n_u) ring.load(a, en, u + (NS - 1) * kWarps, nx, 4);
+                cp_commit();
+            }
+            const uint8_t *sk = my + st * ring.kStage, *sv = sk + U * ROWB;
+            const unsigned have = ring.masks[st];
+            st = st == NS - 1 ? 0 : st + 1;
+            const int j0 = en.first_token(u, U);
+            const bool clear = j0 >= en.lo_max && j0 + U <= en.hi_min && have == (U == 32 ? ~0u : (1u << (U & 31)) - 1);
+            float s[TG][RT];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+                const int r8 = t * NG + g;
+                float2 k[EL / 2], dot[RT];
+#pragma unroll
+                for (int x = 0; x < EL / 4; ++x) {
+                    const float4 v = *reinterpret_cast<const float4*>(sk + at16<ROWB>(r8, e + LT * x));
+                    k[2 * x] = make_float2(v.x, v.y);
+                    k[2 * x + 1] = make_float2(v.z, v.w);
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    dot[r] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < EL / 2; ++x) dot[r] = tc::fma2(qr[r][x], k[x], dot[r]);
+                    s[t][r] = dot[r].x + dot[r].y;
+#pragma unroll
+                    for (int y = LT / 2; y; y >>= 1) s[t][r] += __shfl_xor_sync(0xffffffffu, s[t][r], y);
+                    s[t][r] *= a.scale_log2;
+                }
+                if (!clear) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const int row = en.tile * RT + r;
+                        if (!((have >> r8 & 1) && row < a.nq * a.G &&
+                              paged_visible(paged_bounds(a, en.b, row / a.G), j0 + r8)))
+                            s[t][r] = -INFINITY;
+                    }
+                }
+                if (a.logits && e == 0 && j0 + r8 < a.cap) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const int row = en.tile * RT + r;
+                        if (row < a.nq * a.G)
+                            a.logits[(((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap + j0 + r8] = s[t][r];
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float mn = m[r];
+#pragma unroll
+                for (int t = 0; t < TG; ++t) mn = fmaxf(mn, s[t][r]);
+                if (mn != m[r]) {
+                    const float f = exp2f(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= f;
+#pragma unroll
+                    for (int x = 0; x < EL / 2; ++x) {
+                        o[r][x].x *= f;
+                        o[r][x].y *= f;
+                    }
+                }
+                const float base = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+                for (int t = 0; t < TG; ++t) {
+                    s[t][r] = exp2f(s[t][r] - base);
+                    l[r] += s[t][r];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+                const int r8 = t * NG + g;
+#pragma unroll
+                for (int x = 0; x < EL / 4; ++x) {
+                    const float4 v = *reinterpret_cast<const float4*>(sv + at16<ROWB>(r8, e + LT * x));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float2 p = make_float2(s[t][r], s[t][r]);
+                        o[r][2 * x] = tc::fma2(p, make_float2(v.x, v.y), o[r][2 * x]);
+                        o[r][2 * x + 1] = tc::fma2(p, make_float2(v.z, v.w), o[r][2 * x + 1]);
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+        // join the NG token groups of the warp, then the warps through shared memory
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float M = m[r];
+#pragma unroll
+            for (int y = LT; y < 32; y <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
+            const float f = m[r] == -INFINITY ? 0.f : exp2f(m[r] - M);
+            l[r] *= f;
+#pragma unroll
+            for (int y = LT; y < 32; y <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], y);
+#pragma unroll
+            for (int x = 0; x < EL / 2; ++x) {
+                o[r][x].x *= f;
+                o[r][x].y *= f;
+#pragma unroll
+                for (int y = LT; y < 32; y <<= 1) {
+                    o[r][x].x += __shfl_xor_sync(0xffffffffu, o[r][x].x, y);
+                    o[r][x].y += __shfl_xor_sync(0xffffffffu, o[r][x].y, y);
+                }
+                if (g == 0)
+                    *reinterpret_cast<float2*>(so + (warp * RT + r) * (DP + 4) + (e + LT * (x / 2)) * 4 + 2 * (x & 1)) =
+                        o[r][x];
+            }
+            if (lane == 0) {
+                sm_m[warp * RT + r] = M;
+                sm_l[warp * RT + r] = l[r];
+            }
+        }
+        __syncthreads();
+        paged_finish_segment<kThreads, kWarps, RT>(a, c, sg, so, DP + 4, sm_m, sm_l);
+        __syncthreads();
+        if (!paged_next<false>(a, c, sg)) break;
+    }
+}
+
+template <typename F>
+int launch(F* kern, int smem, const PagedAttnArgs& a, cudaStream_t stream)
+{
+    // per device and idempotent; no state is kept between calls
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return CSA_ERR_CUDA;
+    }
+    launch_pdl(kern, dim3(a.grid), dim3(kThreads), smem, stream, a);
+    return launch_status();
+}
+
+template <int DP, int WR>
+int launch_mma(const PagedAttnArgs& a, cudaStream_t stream)
+{
+    return launch(paged_attn_mma<DP, WR>, MmaShape<DP, WR>::kSmem, a, stream);
+}
+template <int DP, int RT>
+int launch_f32(const PagedAttnArgs& a, cudaStream_t stream)
+{
+    return launch(paged_attn_f32<DP, RT>, F32Shape<DP, RT>::kSmem, a, stream);
+}
+
+}  // namespace
+
+// Rows, units and CTAs of a decode call.
+PagedShape paged_decode_shape(int dtype, int rows, int d)
+{
+    PagedShape s{};
+    s.DP = d <= 64 ? 64 : d <= 128 ? 128 : 256;
+    if (dtype == CSA_BF16) {
+        s.kind = kPagedMma;
+        s.WR = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        s.R = 16 * s.WR;
+        s.unit = s.DP == 64 || (s.WR > 1 && s.DP == 128) ? 32 : 16;
+        s.min_units = 2 * (kWarps / s.WR);
+        s.grid = (s.DP == 256 && s.WR == 1 ? 1 : 2) * kNumSMs;
+    } else {
+        s.kind = kPagedF32;
+        s.WR = s.R = rows <= 4 ? 4 : 8;
+        s.unit = 1024 / s.DP;
+        s.min_units = 2 * kWarps;
+        s.grid = 2 * kNumSMs;
+    }
+    return s;
+}
+
+int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream)
+{
+    if (s.kind == kPagedF32) {
+        if (s.DP == 64) return s.WR == 4 ? launch_f32<64, 4>(a, stream) : launch_f32<64, 8>(a, stream);
+        if (s.DP == 128) return s.WR == 4 ? launch_f32<128, 4>(a, stream) : launch_f32<128, 8>(a, stream);
+        return s.WR == 4 ? launch_f32<256, 4>(a, stream) : launch_f32<256, 8>(a, stream);
+    }
+#define PAGED_MMA(DP) \
+    (s.WR == 1 ? launch_mma<DP, 1>(a, stream) : s.WR == 2 ? launch_mma<DP, 2>(a, stream) : launch_mma<DP, 4>(a, stream))
+    if (s.DP == 64) return PAGED_MMA(64);
+    if (s.DP == 128) return PAGED_MMA(128);
+    return PAGED_MMA(256);
+#undef PAGED_MMA
+}
+
+}  // namespace csa
