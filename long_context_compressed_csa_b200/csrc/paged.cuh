@@ -45,9 +45,12 @@ struct PagedAttnArgs {
     int R, n_tiles;
     int unit;              // cached tokens of a schedule unit
     int min_units;         // units a CTA takes at least
+    int item_units;        // what an item costs beside its units, in units
     int grid;              // CTAs launched
     // workspace
-    int4* desc;            // [grid]: the split item that begins in this CTA {entry, head, last CTA, -}, entry -1: none
+    uint32_t* status;      // 1 after a timeout
+    int4* desc;            // [grid]: the split item that begins in this CTA {entry, head, last CTA, 1 after a timeout},
+                           // entry -1: none
     float* part_o;         // [2 * grid][R][d] unnormalised partial outputs
     float2* part_ml;       // [2 * grid][R] their (running maximum, sum), base 2
     // accumulated weights: scaled base-2 logits [B][n_kv][nq * G][cap] and the final base-2
@@ -120,15 +123,15 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
     return r;
 }
 
-// Units of entry e (0 past the last one).  All lanes of a warp call it, lane l with e = e0 + l.
+// Places of entry e in the list of a key head (0 past the last one).  All lanes of a warp call it, lane l with e = e0 + l.
 template <bool COOP>
 CSA_DEV int paged_units(const PagedAttnArgs& a, int e, int NB)
 {
-    if (!COOP) return e < NB ? paged_entry<false>(a, e).n : 0;
+    if (!COOP) return e < NB ? paged_entry<false>(a, e).n + a.item_units : 0;
     int n = 0;
     const int lane = threadIdx.x & 31, e0 = e - lane;
     for (int k = 0; k < 32 && e0 + k < NB; ++k) {
-        const int m = paged_entry<true>(a, e0 + k).n;
+        const int m = paged_entry<true>(a, e0 + k).n + a.item_units;
         if (lane == k) n = m;
     }
     return n;
@@ -136,14 +139,16 @@ CSA_DEV int paged_units(const PagedAttnArgs& a, int e, int NB)
 
 // The schedule.  The units of all items, in the order (entry, key head, unit), are one list
 // that is cut into equal runs, one for each CTA, whatever the sequences' lengths: a ragged
-// batch and one long sequence both fill the GPU.  Only the first and the last item of a run
+// batch and one long sequence both fill the GPU.  An item begins with item_units places
+// that hold no unit: what it costs to begin and end one, so that a run of many short items (the first
+// rows of a prompt) is no longer than one of few long ones.  Only the first and the last item of a run
 // can be cut, so a CTA writes at most two partial results; paged_attn_combine joins them in
 // the order of the CTAs.  The lengths are read on the device, so a captured graph follows them.
 struct PagedCursor {
     int64_t at, end;       // this CTA's run of the list
     int64_t W;
     int ctas;              // CTAs that have a run
-    int e, h, u;           // entry, key head and unit within the item of `at`
+    int e, h, u;           // entry, key head and place within the item of `at`
     PagedEntry en;
 };
 
@@ -192,7 +197,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedC
             if (w == warp) inc += all;
             all += sh[w];
         }
-        // inc: units (of one key head) up to and with entry e
+        // inc: places (of one key head) up to and with entry e
         if (n > 0 && (inc - n) * a.n_kv <= c.at && c.at < inc * a.n_kv) {
             sh[T / 32] = e;
             sh[T / 32 + 1] = inc - n;
@@ -204,38 +209,44 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedC
     c.e = (int)sh[T / 32];
     const int64_t off = c.at - sh[T / 32 + 1] * a.n_kv;
     c.en = paged_entry<COOP>(a, c.e);
-    c.h = (int)(off / c.en.n);
-    c.u = (int)(off - (int64_t)c.h * c.en.n);
+    const int places = c.en.n + a.item_units;
+    c.h = (int)(off / places);
+    c.u = (int)(off - (int64_t)c.h * places);
     __syncthreads();  // sh may be reused
     return true;
 }
 
 // The part of the current item that this CTA has, and where its result goes.
 struct PagedSegment {
-    int u0, u1;
+    int places;
+    int u0, u1;  // units; empty where the run ends before the item's first unit
     bool whole;
-    int slot;  // of a partial result
+    int slot;    // of a partial result
 };
-// Called by one thread when an item's first part is partial: the combine's description of it.
 CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c, int cta)
 {
     PagedSegment s;
-    s.u0 = c.u;
-    s.u1 = (int)min((int64_t)c.en.n, c.u + (c.end - c.at));
+    const int all = c.en.n + a.item_units, p1 = (int)min((int64_t)all, c.u + (c.end - c.at));
+    s.places = p1 - c.u;
+    s.u0 = max(0, c.u - a.item_units);
+    s.u1 = max(0, p1 - a.item_units);
     s.whole = s.u0 == 0 && s.u1 == c.en.n;
     s.slot = 2 * cta + (s.u0 == 0 ? 1 : 0);
-    if (!s.whole && s.u0 == 0 && threadIdx.x == 0) {
-        // the run that has the item's last unit: unit x lies in run ((x + 1) ctas - 1) / W
-        const int64_t last = c.at + c.en.n - 1;
-        a.desc[cta] = make_int4(c.e, c.h, (int)(((last + 1) * c.ctas - 1) / c.W), 0);
-    }
     return s;
+}
+// The combine's description of an item whose first units, but not its last, are this CTA's.  One thread.
+CSA_DEV void paged_describe(const PagedAttnArgs& a, const PagedCursor& c, const PagedSegment& s, int cta)
+{
+    if (s.whole || s.u0 > 0 || s.u1 == 0) return;
+    // the run that has the item's last unit: place x lies in run ((x + 1) ctas - 1) / W
+    const int64_t last = c.at - c.u + c.en.n + a.item_units - 1;
+    a.desc[cta] = make_int4(c.e, c.h, (int)(((last + 1) * c.ctas - 1) / c.W), 0);
 }
 // On to the next item; false at the end of the run.
 template <bool COOP>
 CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegment& s)
 {
-    c.at += s.u1 - s.u0;
+    c.at += s.places;
     if (c.at >= c.end) return false;
     c.u = 0;
     if (++c.h == a.n_kv) {
@@ -307,14 +318,18 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
 }
 
 // Which kernel a call runs on, its row tile, and the units and CTAs of its schedule.
-enum PagedKind { kPagedSimt, kPagedMma, kPagedF32 };
+enum PagedKind { kPagedSimt, kPagedMma, kPagedF32, kPagedPrompt };
 struct PagedShape {
     PagedKind kind;
     int DP;         // head width rounded up to a kernel's
     int WR;         // kPagedMma: row groups of 16; kPagedF32: rows
-    int R, unit, min_units, grid;
+    int R, unit, min_units, item_units, grid;
 };
 PagedShape paged_decode_shape(int dtype, int rows, int d);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream);
+
+bool paged_prompt_takes(const PagedPool& pl, int n_kv, int d);
+PagedShape paged_prompt_shape(int d);
+int launch_paged_prompt(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream);
 
 }  // namespace csa

@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
     const T* V = static_cast<const T*>(a.V);
     while (true) {
         const PagedSegment sg = paged_segment(a, c, cta);
+        if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
+        if (tid == 0) paged_describe(a, c, sg, cta);
         const PagedEntry en = c.en;
         for (int x = tid; x < R * d; x += kSimtThreads) {
             const int64_t o = paged_out_row(a, en.b, en.tile, c.h, x / d);
@@ -138,60 +140,75 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
     }
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-// One CTA per (split item, row): joins the partial results of the CTAs that had a part of it.
+// Joins the partial results of the CTAs that had a part of an item: PS warps of a CTA share the pieces
+// of a row.  A decode call may cut an item into many pieces and has few rows (PS = 4); a prompt's
+// items are cut in two or three and have many (PS = 1).
+template <int PS>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs a)
 {
-    __shared__ float sh[kJoinThreads / 32][2];
-    __shared__ float so[kJoinThreads / 32][kPagedMaxD];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c0 = blockIdx.x, r = blockIdx.y;
+    constexpr int NC = kPagedMaxD / 32, RW = kJoinWarps / PS;
+    __shared__ float sh[kJoinWarps][2];
+    __shared__ float so[PS > 1 ? kJoinWarps : 1][kPagedMaxD];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c0 = blockIdx.x;
+    const int r = blockIdx.y * RW + warp / PS, ps = warp % PS;
     pdl_launch_dependents();
     pdl_wait();
+    if (c0 == 0 && blockIdx.y == 0 && warp == 0) {
+        int late = 0;
+        for (int i = lane; i < a.grid; i += 32) late |= a.desc[i].w;
+        late = __any_sync(0xffffffffu, late);
+        if (lane == 0) *a.status = late ? 1u : 0u;
+    }
     const int4 ds = a.desc[c0];
     if (ds.x < 0) return;
     const int b = ds.x / a.n_tiles, tile = ds.x - b * a.n_tiles, h = ds.y;
-    const int64_t o = paged_out_row(a, b, tile, h, r);
-    if (o < 0) return;
     const int np = ds.z - c0 + 1;
+    const bool in = r < paged_rows(a, tile);
     // piece p lies in slot 2 c0 + 1 for p = 0, 2 (c0 + p) after that
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * a.R + r; };
-    float M = -INFINITY;
-    for (int p = tid; p < np; p += kJoinThreads) M = fmaxf(M, a.part_ml[slot(p)].x);
+    float M = -INFINITY, L = 0.f, acc[NC];
+    if (in)
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if (lane == 0) sh[warp][0] = M;
-    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, sh[w][0]);
-    float L = 0.f, acc[kPagedMaxD / 32];
+    for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+    if (in) {
+#pragma unroll 2
+        for (int p = ps; p < np; p += PS) {
+            const float2 ml = a.part_ml[slot(p)];
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            L = fmaf(w, ml.y, L);
+            const float* src = a.part_o + slot(p) * a.d;
 #pragma unroll
-    for (int i = 0; i < kPagedMaxD / 32; ++i) acc[i] = 0.f;
-    for (int p = warp; p < np; p += kJoinThreads / 32) {
-        const float2 ml = a.part_ml[slot(p)];
-        if (ml.x == -INFINITY) continue;
-        const float w = exp2f(ml.x - M);
-        L = fmaf(w, ml.y, L);
-        const float* src = a.part_o + slot(p) * a.d;
-#pragma unroll
-        for (int i = 0; i < kPagedMaxD / 32; ++i)
-            if (lane + 32 * i < a.d) acc[i] = fmaf(w, src[lane + 32 * i], acc[i]);
+            for (int i = 0; i < NC; ++i)
+                if (lane + 32 * i < a.d) acc[i] = fmaf(w, src[lane + 32 * i], acc[i]);
+        }
     }
-    if (lane == 0) sh[warp][1] = L;
+    const int64_t o = in ? paged_out_row(a, b, tile, h, r) : -1;
+    if (PS > 1) {
+        if (lane == 0) sh[warp][0] = L;
 #pragma unroll
-    for (int i = 0; i < kPagedMaxD / 32; ++i)
-        if (lane + 32 * i < a.d) so[warp][lane + 32 * i] = acc[i];
-    __syncthreads();
-    L = 0.f;
+        for (int i = 0; i < NC; ++i)
+            if (lane + 32 * i < a.d) so[warp][lane + 32 * i] = acc[i];
+        __syncthreads();
+        if (ps > 0) return;
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) L += sh[w][1];
-    for (int x = tid; x < a.d; x += kJoinThreads) {
-        float v = 0.f;
+        for (int w = 1; w < PS; ++w) {
+            L += sh[warp + w][0];
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) v += so[w][x];
-        paged_store(a, o * a.d + x, L > 0.f ? v / L : 0.f);
+            for (int i = 0; i < NC; ++i)
+                if (lane + 32 * i < a.d) acc[i] += so[warp + w][lane + 32 * i];
+        }
     }
-    if (tid == 0) paged_store_lse(a, o, b, tile, h, r, M, L);
+    if (o < 0) return;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        if (lane + 32 * i < a.d) paged_store(a, o * a.d + lane + 32 * i, acc[i] * inv);
+    if (lane == 0) paged_store_lse(a, o, b, tile, h, r, M, L);
 }
 
 constexpr int kWeightThreads = 256;
@@ -223,15 +240,20 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
 
 }  // namespace
 
-// The kernel of a call.  The CUDA-core kernel takes what the others cannot load 16 bytes at a time.
-static PagedShape paged_shape(int dtype, bool wide, int rows, int d)
+// The kernel of a call, by its rows (queries x heads of a key head), type and layout.  `wide`: every
+// row can be loaded 16 bytes at a time; what cannot takes the CUDA-core kernel.  `boxes`: the pools can be
+// read by TMA.  A tile of 128 rows costs the prompt kernel the same however few of them there are.
+constexpr int kPromptRows = 17;
+static PagedShape paged_shape(int dtype, bool wide, bool boxes, int rows, int d)
 {
+    if (wide && boxes && dtype == CSA_BF16 && rows >= kPromptRows && d <= 128) return paged_prompt_shape(d);
     if (wide) return paged_decode_shape(dtype, rows, d);
     PagedShape s{};
     s.kind = kPagedSimt;
     s.R = kSimtRows;
     s.unit = kSimtUnit;
     s.min_units = kSimtWarps;
+    s.item_units = 2;
     s.grid = 2 * kNumSMs;
     return s;
 }
@@ -246,8 +268,8 @@ static PagedPlan paged_plan(int B, int nq, int G, int n_kv, int d, int64_t cap, 
     PagedPlan p{};
     size_t slots = 0;  // rows of partial results
     for (int dtype : {CSA_BF16, CSA_F32})
-        for (bool wide : {false, true}) {
-            const PagedShape s = paged_shape(dtype, wide, nq * G, d);
+        for (int way = 0; way < 3; ++way) {
+            const PagedShape s = paged_shape(dtype, way > 0, way > 1, nq * G, d);
             slots = std::max(slots, (size_t)2 * s.grid * s.R);
         }
     size_t at = 256 + align_up(sizeof(int4) * kPagedMaxCtas, 256);
@@ -314,13 +336,14 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     // 16-byte loads: every row starts on a 16-byte boundary and is whole 16-byte words
     const int64_t lds = pool_ld_page | pool_ld_row | (n_kv > 1 ? pool_ld_head : 0) | d;
     const bool wide = aligned16(q) && aligned16(K) && aligned16(V) && lds * elem_bytes(dtype) % 16 == 0;
-    const PagedShape sp = paged_shape(dtype, wide, nq * G, d);
-    a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units;
+    const PagedShape sp = paged_shape(dtype, wide, paged_prompt_takes(pl, n_kv, d), nq * G, d);
+    a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units; a.item_units = sp.item_units;
     a.n_tiles = (nq * G + sp.R - 1) / sp.R;
     // no more CTAs than the capacity has units
     const int64_t units = std::max<int64_t>(1, (cap + sp.unit - 1) / sp.unit) * B * n_kv * a.n_tiles;
     a.grid = (int)std::max<int64_t>(1, std::min<int64_t>(sp.grid, units / sp.min_units));
     char* ws = static_cast<char*>(workspace);
+    a.status = reinterpret_cast<uint32_t*>(ws);
     a.desc = reinterpret_cast<int4*>(ws + 256);
     a.part_ml = reinterpret_cast<float2*>(ws + p.part_ml);
     a.part_o = reinterpret_cast<float*>(ws + p.part_o);
@@ -340,10 +363,14 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
             launch_pdl(paged_attn_simt<float>, dim3(a.grid), dim3(kSimtThreads), smem, s, a);
         st = launch_status();
     } else {
-        st = launch_paged_decode(a, sp, s);
+        st = sp.kind == kPagedPrompt ? launch_paged_prompt(a, sp, s) : launch_paged_decode(a, sp, s);
     }
     if (st != CSA_OK) return st;
-    launch_pdl(paged_attn_combine, dim3(a.grid, std::min(a.R, nq * G)), dim3(kJoinThreads), 0, s, a);
+    const int rows = std::min(a.R, nq * G);
+    if (sp.kind == kPagedPrompt)
+        launch_pdl(paged_attn_combine<1>, dim3(a.grid, (rows + 7) / 8), dim3(kJoinThreads), 0, s, a);
+    else
+        launch_pdl(paged_attn_combine<4>, dim3(a.grid, (rows + 1) / 2), dim3(kJoinThreads), 0, s, a);
     st = launch_status();
     if (st != CSA_OK || !acc || cap == 0) return st;
     launch_pdl(paged_weights_kernel, dim3((unsigned)((cap + kWeightThreads - 1) / kWeightThreads), n_kv, B),

@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
     const int r0 = wr * 16 + (lane >> 2);  // this lane's rows: r0 and r0 + 8
     while (true) {
         const PagedSegment sg = paged_segment(a, c, cta);
+        if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
+        if (tid == 0) paged_describe(a, c, sg, cta);
         const PagedEntry en = c.en;
         ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
         ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
     const float* q = static_cast<const float*>(a.q);
     while (true) {
         const PagedSegment sg = paged_segment(a, c, cta);
+        if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
+        if (tid == 0) paged_describe(a, c, sg, cta);
         const PagedEntry en = c.en;
         ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 4;
         ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 4;
@@ -553,12 +557,14 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
         s.R = 16 * s.WR;
         s.unit = s.DP == 64 || (s.WR > 1 && s.DP == 128) ? 32 : 16;
         s.min_units = 2 * (kWarps / s.WR);
+        s.item_units = s.WR == 1 ? 8 : 4;
         s.grid = (s.DP == 256 && s.WR == 1 ? 1 : 2) * kNumSMs;
     } else {
         s.kind = kPagedF32;
         s.WR = s.R = rows <= 4 ? 4 : 8;
         s.unit = 1024 / s.DP;
         s.min_units = 2 * kWarps;
+        s.item_units = 8;
         s.grid = 2 * kNumSMs;
     }
     return s;

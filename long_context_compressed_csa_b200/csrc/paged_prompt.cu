@@ -1,0 +1,479 @@
+// paged_attn for many query rows: a prompt, a chunk of one, or a decode step whose query rows fill a tile.
+//
+// Packed rows (query, head of the key head's group) are the M dimension of tcgen05: both products
+//   S = Q K^T (128 rows x 128 tokens)   and   O += P V (128 rows x d)
+// are bf16 tensor-core work with fp32 accumulators in TMEM.  A CTA has two tiles of 128 rows
+// that share every K and V tile, and takes a run of the schedule (paged.cuh):
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread per row: S from TMEM to registers,
+//                   running maximum and sum, P (bf16) over S in TMEM; q -> shared memory before, O ->
+//                   memory after a segment
+//   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
+//                   not there, or that no row sees, is a box outside the tensor: zeros
+//   warp 9          MMA issue: while one tile's softmax runs, the other tile's products do
+// O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8): S(j) is
+// issued after P(j-1) V, so once S(j) is there O is at rest, and the softmax thread rescales its
+// row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
+// operand of the tensor core has to be; the row sum takes the weights before the rounding.
+// The masks (positions, window, first tokens, missing pages) are applied to S only in units that
+// are not wholly visible; there the rows of V that no query sees are set to zero too, since 0 x NaN
+// would reach the sums.  Bounded waits: a timeout ends the CTA and sets its status.
+#include "paged.cuh"
+#include "tc_utils.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kM = 128;             // rows of a tile
+constexpr int kT = 128;             // cached tokens of a unit
+constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
+constexpr int kRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
+constexpr float kRescale = 8.0f;    // log2 units
+
+template <int DP>
+struct PromptShape {
+    static constexpr int kPanels = DP / 64;
+    static constexpr int kTile = kT * DP * 2;           // bytes of a K or V tile (and of a q tile)
+    static constexpr int kStages = DP == 64 ? 4 : 2;
+    static constexpr int kSmem = 1024 + 2 * kTile + 2 * kStages * kTile;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A: two values a 32-bit column), fp32 accumulate.
+CSA_DEV void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+CSA_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+CSA_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int r, int p)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(h), "r"(r), "r"(p)
+        : "memory");
+}
+CSA_DEV uint32_t pack2(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                  const __grid_constant__ PagedAttnArgs a, const int box_rows)
+{
+    using S = PromptShape<DP>;
+    constexpr int NS = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* sQ = smem;                    // two tiles
+    uint8_t* sK = smem + 2 * S::kTile;     // [NS]
+    uint8_t* sV = sK + NS * S::kTile;      // [NS]
+    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
+    __shared__ uint32_t have[NS];          // of a V stage: bit i: rows 8 i .. 8 i + 7 have a page
+    __shared__ uint32_t tmem_slot;
+    __shared__ int64_t sh[kThreads / 32 + 2];
+    __shared__ volatile int failed;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&Qfull[i], kM);
+            tc::mbar_init(&Sfull[i], 1);
+            tc::mbar_init(&Pready[i], kM);
+            tc::mbar_init(&Ofull[i], 1);
+        }
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&Kfull[i], 1);
+            tc::mbar_init(&Kempty[i], 1);
+            tc::mbar_init(&Vfull[i], 1);
+            tc::mbar_init(&Vempty[i], 1);
+        }
+        failed = 0;
+        tc::tma_prefetch_desc(&map_k);
+        tc::tma_prefetch_desc(&map_v);
+        tc::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    // S of tile w at column w kT, O at 2 kT + w DP
+    auto tS = [&](int w) { return tmem + w * kT; };
+    auto tO = [&](int w) { return tmem + 2 * kT + w * DP; };
+    pdl_wait();
+    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+    PagedCursor c;
+    const bool some = paged_schedule<kThreads, true>(a, cta, sh, c);
+    // false after a timeout; the caller leaves its loops
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (tc::mbar_wait(bar, phase & 1, tc::kWaitBudget)) return true;
+        failed = 1;
+        return false;
+    };
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };  // a warp gives up as one
+
+    if (some && warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ------------------------------------------------------------ softmax
+        const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
+        uint32_t n_s = 0, n_q = 0, n_v = 0;  // phases passed: S of this tile, segments of this tile, V tiles
+        bool ok = true;
+        while (ok) {
+            const PagedSegment sg = paged_segment(a, c, cta);
+            if (sg.u0 == sg.u1) break;
+            if (tid == 0) paged_describe(a, c, sg, cta);
+            const PagedEntry en = c.en;
+            const int row = en.tile * a.R + w * kM + r, n_rows = paged_rows(a, en.tile);
+            if (w * kM < n_rows) {
+                const bool in = w * kM + r < n_rows;
+                const int64_t at = in ? paged_out_row(a, en.b, en.tile, c.h, w * kM + r) : 0;
+                const RowBounds rb = in ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
+                {
+                    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at * a.d);
+#pragma unroll
+                    for (int x = 0; x < DP / 8; ++x) {
+                        const uint4 v = in && x * 8 < a.d ? q[x] : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sQ + w * S::kTile + (x >> 3) * (kM * 128) +
+                                                  tc::sw128_offset(r, x & 7)) = v;
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&Qfull[w]);
+                }
+                float* lg = a.logits && in
+                                ? a.logits + (((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap
+                                : nullptr;
+                float m = -INFINITY, l = 0.f;  // m: what the weights in O and l are relative to
+                for (int u = sg.u0; u < sg.u1 && ok; ++u, ++n_s) {
+                    const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
+                    ok = all(wait(&Vfull[vs], vt / NS)) && all(wait(&Sfull[w], n_s));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(s_at + 32 * i, s[i]);
+                    const int j0 = en.first_token(u, kT);
+                    const uint32_t hv = have[vs];
+                    const bool clear = j0 >= en.lo_max && j0 + kT <= en.hi_min && hv == 0xffffu;
+                    if (!clear) {
+                        // rows of V that no query sees: thread r has row r of the tile
+                        const int j = j0 + r;
+                        if (!en.seen(j)) {
+#pragma unroll
+                            for (int x = 0; x < DP / 8; ++x)
+                                *reinterpret_cast<uint4*>(sV + vs * S::kTile + (x >> 3) * (kT * 128) +
+                                                          tc::sw128_offset(r, x & 7)) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);
+                    if (!clear) {
+#pragma unroll
+                        for (int i = 0; i < kT; ++i)
+                            if (!((hv >> (i >> 3) & 1) && paged_visible(rb, j0 + i)))
+                                s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+                    }
+                    if (lg) {
+#pragma unroll
+                        for (int i = 0; i < kT; ++i)
+                            if (j0 + i < a.cap) lg[j0 + i] = __uint_as_float(s[i >> 5][i & 31]) * a.scale_log2;
+                    }
+                    __syncwarp();
+                    float top = -INFINITY;
+                    {
+                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < kT; i += 4)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                t4[x] = fmaxf(t4[x], __uint_as_float(s[i >> 5][(i + x) & 31]));
+                        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.scale_log2;
+                    }
+                    const bool grow = top > m + kRescale;  // m = -inf: as soon as anything is visible
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? exp2f(m - top) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (u > sg.u0) {  // before the first product O holds nothing of this segment
+#pragma unroll 1
+                            for (int x = 0; x < DP; x += 32) {
+                                uint32_t o[32];
+                                tc::tmem_ld32_async(o_at + x, o);
+                                tc::tmem_wait_ld_regs(o);
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                                tmem_st32(o_at + x, o);
+                            }
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    const float2 sc = make_float2(a.scale_log2, a.scale_log2), sb = make_float2(neg, neg);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int e = half * 64 + 2 * i;
+                            float2 x = tc::fma2(make_float2(__uint_as_float(s[e >> 5][e & 31]),
+                                                            __uint_as_float(s[e >> 5][(e + 1) & 31])), sc, sb);
+                            x.x = tc::ex2_approx(x.x);
+                            x.y = tc::ex2_approx(x.y);
+                            sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
+                            p[i] = pack2(x.x, x.y);
+                        }
+                        tmem_st32(s_at + half * 32, p);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&Pready[w]);
+                }
+                if (ok) ok = all(wait(&Ofull[w], n_q));
+                if (ok) {
+                    tc::fence_after_sync();
+                    const int64_t slot = (int64_t)sg.slot * a.R + w * kM + r;
+                    const float inv = sg.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+#pragma unroll
+                    for (int x = 0; x < DP; x += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32_async(o_at + x, o);
+                        tc::tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8) {
+                            if (!in || x + y >= a.d) continue;
+                            float v[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[y + z]) * inv;
+                            if (sg.whole && a.out_bf16) {
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * a.d + x + y) =
+                                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+                            } else {
+                                float4* to = reinterpret_cast<float4*>(
+                                    sg.whole ? static_cast<float*>(a.out) + at * a.d + x + y : a.part_o + slot * a.d + x + y);
+                                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (in) {
+                        if (sg.whole)
+                            paged_store_lse(a, at, en.b, en.tile, c.h, w * kM + r, m, l);
+                        else
+                            a.part_ml[slot] = make_float2(m, l);
+                    }
+                    tc::fence_before_sync();  // these loads, before the next segment's products write O
+                }
+                ++n_q;
+            }
+            n_v += (uint32_t)(sg.u1 - sg.u0);
+            if (!ok || !paged_next<true>(a, c, sg)) break;
+        }
+    } else if (some) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    }
+    if (some && warp == kLoadWarp) {
+        // ------------------------------------------------------------ K and V
+        uint32_t n = 0;  // tiles begun
+        bool ok = true;
+        const int boxes = kT / box_rows, none = (int)a.pl.n_pages;
+        while (ok) {
+            const PagedSegment sg = paged_segment(a, c, cta);
+            if (sg.u0 == sg.u1) break;
+            for (int u = sg.u0; u < sg.u1; ++u, ++n) {
+                const int j = c.en.first_token(u, kT) + lane * box_rows;
+                int page = none, in = 0;
+                const bool any = j < c.en.hi_max && (j < c.en.sink || j + box_rows > c.en.lo_min);
+                if (lane < boxes && any && j < a.cap) {
+                    const int p = j / a.pl.page;
+                    const int id = a.pl.table[(int64_t)c.en.b * a.pl.max_pages + p];
+                    if ((uint32_t)id < (uint32_t)none) {
+                        page = id;
+                        in = j - p * a.pl.page;
+                    }
+                }
+                const unsigned there = __ballot_sync(0xffffffffu, page != none);
+                uint32_t hv = 0;
+                for (int i = 0; i < kT / 8; ++i) hv |= (there >> (i * 8 / box_rows) & 1u) << i;
+                const uint32_t st = n % NS, ph = n / NS + 1;  // waits of the first round pass at once
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint64_t *full = kv ? &Vfull[st] : &Kfull[st], *empty = kv ? &Vempty[st] : &Kempty[st];
+                    ok = all(wait(empty, ph));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (kv) have[st] = hv;
+                        tc::mbar_arrive_expect_tx(full, S::kTile);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        uint8_t* dst = (kv ? sV : sK) + st * S::kTile + lane * box_rows * 128;
+#pragma unroll
+                        for (int x = 0; x < S::kPanels; ++x)
+                            tma_load_4d(dst + x * (kT * 128), kv ? &map_v : &map_k, full, x * 64, c.h, in, page);
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok || !paged_next<true>(a, c, sg)) break;
+        }
+        // no copy is in flight when the CTA ends: on the normal path the products have waited for them
+        if (!ok)
+            for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k) {
+                wait(&Kfull[k % NS], k / NS);
+                wait(&Vfull[k % NS], k / NS);
+            }
+    } else if (some && warp == kMmaWarp) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
+        constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kM, DP, false, true);
+        uint32_t n = 0;                     // tiles used
+        uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};
+        bool ok = true;
+        const uint32_t q0 = tc::smem_u32(sQ), k0 = tc::smem_u32(sK), v0 = tc::smem_u32(sV);
+        auto mma_s = [&](int w, uint32_t st) {
+#pragma unroll
+            for (int x = 0; x < DP / 16; ++x) {
+                const uint32_t at = (x >> 2) * (kM * 128) + (x & 3) * 32;
+                tc::mma_bf16_ss(tS(w), tc::smem_desc_sw128(q0 + w * S::kTile + at, 16, 1024),
+                                tc::smem_desc_sw128(k0 + st * S::kTile + at, 16, 1024), kIdescS, x ? 1u : 0u);
+            }
+        };
+        auto mma_o = [&](int w, uint32_t st, bool more) {
+#pragma unroll
+            for (int x = 0; x < kT / 16; ++x)
+                mma_bf16_ts(tO(w), tS(w) + x * 8,
+                            tc::smem_desc_sw128(v0 + st * S::kTile + x * 16 * 128, kT * 128, 1024), kIdescO,
+                            more || x ? 1u : 0u);
+        };
+        while (ok) {
+            const PagedSegment sg = paged_segment(a, c, cta);
+            if (sg.u0 == sg.u1) break;
+            const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1, n_u = sg.u1 - sg.u0;
+            if (lane == 0) {
+                ok = wait(&Kfull[n % NS], n / NS);
+                for (int w = 0; w < tiles && ok; ++w) {
+                    ok = wait(&Qfull[w], n_q[w]++);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    mma_s(w, n % NS);
+                    tc::mma_commit(&Sfull[w]);
+                }
+                if (ok) tc::mma_commit(&Kempty[n % NS]);
+                for (int u = 0; u < n_u && ok; ++u, ++n) {
+                    const uint32_t st = n % NS, nx = (n + 1) % NS;
+                    ok = wait(&Vfull[st], n / NS);
+                    for (int w = 0; w < tiles && ok; ++w) {
+                        ok = wait(&Pready[w], n_p[w]++);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        mma_o(w, st, u > 0);
+                        if (u + 1 < n_u) {
+                            if (w == 0) ok = wait(&Kfull[nx], (n + 1) / NS);
+                            if (!ok) break;
+                            mma_s(w, nx);
+                            tc::mma_commit(&Sfull[w]);
+                        } else {
+                            tc::mma_commit(&Ofull[w]);
+                        }
+                    }
+                    if (!ok) break;
+                    tc::mma_commit(&Vempty[st]);
+                    if (u + 1 < n_u) tc::mma_commit(&Kempty[nx]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            n = __shfl_sync(0xffffffffu, n, 0);
+            if (!ok || !paged_next<true>(a, c, sg)) break;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && failed) a.desc[cta].w = 1;
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DP>
+int launch(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box_rows, cudaStream_t stream)
+{
+    constexpr int smem = PromptShape<DP>::kSmem;
+    if (cudaFuncSetAttribute(paged_attn_prompt<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return CSA_ERR_CUDA;
+    }
+    launch_pdl(paged_attn_prompt<DP>, dim3(a.grid), dim3(kThreads), smem, stream, k, v, a, box_rows);
+    return launch_status();
+}
+
+}  // namespace
+
+bool paged_prompt_takes(const PagedPool& pl, int n_kv, int d)
+{
+    // TMA: boxes of 8 rows or more that lie in one page, strides that a tensor map can hold
+    constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements
+    return d <= 128 && pl.page % 8 == 0 && pl.n_pages >= 1 && pl.n_pages < INT32_MAX &&
+           (pl.n_pages == 1 || pl.ld_page > 0) && pl.ld_page < kMaxStride && pl.ld_row < kMaxStride &&
+           (n_kv == 1 || pl.ld_head < kMaxStride);
+}
+
+PagedShape paged_prompt_shape(int d)
+{
+    PagedShape s{};
+    s.kind = kPagedPrompt;
+    s.DP = d <= 64 ? 64 : 128;
+    s.R = 2 * kM;
+    s.unit = kT;
+    s.min_units = 2;
+    s.item_units = 2;
+    s.grid = kNumSMs;
+    return s;
+}
+
+int launch_paged_prompt(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream)
+{
+    const PagedPool& pl = a.pl;
+    int rows = 128;  // of a box: the largest power of two that divides the page
+    while (pl.page % rows) rows >>= 1;
+    // strides of dimensions of size 1 are never used, but have to be valid
+    const int64_t ld_head = a.n_kv > 1 ? pl.ld_head : align_up(a.d, 8);
+    const int64_t ld_page = pl.n_pages > 1 ? pl.ld_page : pl.ld_row;
+    CUtensorMap k, v;
+    for (int i = 0; i < 2; ++i)
+        if (!make_tmap_bf16_4d(i ? &v : &k, i ? a.V : a.K, a.d, a.n_kv, pl.page, pl.n_pages, ld_head, pl.ld_row, ld_page,
+                               64, rows))
+            return CSA_ERR_CUDA;
+    return s.DP == 64 ? launch<64>(a, k, v, rows, stream) : launch<128>(a, k, v, rows, stream);
+}
+
+}  // namespace csa

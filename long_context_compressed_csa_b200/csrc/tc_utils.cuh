@@ -345,6 +345,10 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
 // row, a multiple of 16).
 bool make_tmap_bf16_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                              uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows);
+// Host: a 4-D bf16 tensor map [n3][n2][n1][cols] (strides in elements, multiples of 8) with a box of
+// box_cols x 1 x box_n2 x 1 and 128-byte swizzle.
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t n3,
+                       uint64_t ld1, uint64_t ld2, uint64_t ld3, uint32_t box_cols, uint32_t box_n2);
 // Same for a 2-D tensor of bytes (E4M3 codes).
 bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                      uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows);

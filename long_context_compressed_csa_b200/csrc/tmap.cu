@@ -57,6 +57,21 @@ bool make_tmap_bf16_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, 
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t n3,
+                       uint64_t ld1, uint64_t ld2, uint64_t ld3, uint32_t box_cols, uint32_t box_n2)
+{
+    EncodeTiled fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {cols, n1, n2, n3};
+    cuuint64_t strides[3] = {ld1 * 2, ld2 * 2, ld3 * 2};
+    cuuint32_t box[4] = {box_cols, 1, box_n2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                      uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows)
 {
