@@ -123,20 +123,6 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
     return r;
 }
 
-// Places of entry e in the list of a key head (0 past the last one).  All lanes of a warp call it, lane l with e = e0 + l.
-template <bool COOP>
-CSA_DEV int paged_units(const PagedAttnArgs& a, int e, int NB)
-{
-    if (!COOP) return e < NB ? paged_entry<false>(a, e).n + a.item_units : 0;
-    int n = 0;
-    const int lane = threadIdx.x & 31, e0 = e - lane;
-    for (int k = 0; k < 32 && e0 + k < NB; ++k) {
-        const int m = paged_entry<true>(a, e0 + k).n + a.item_units;
-        if (lane == k) n = m;
-    }
-    return n;
-}
-
 // The schedule.  The units of all items, in the order (entry, key head, unit), are one list
 // that is cut into equal runs, one for each CTA, whatever the sequences' lengths: a ragged
 // batch and one long sequence both fill the GPU.  An item begins with item_units places
@@ -152,16 +138,41 @@ struct PagedCursor {
     PagedEntry en;
 };
 
-// T threads call it together; sh has T / 32 + 2 elements.  False: this CTA has no run.
+// Shared memory of paged_schedule.
 template <int T, bool COOP>
-CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedCursor& c)
+struct PagedScratch {
+    int64_t sums[T / 32 + 2];
+    int places[COOP ? T : 1];
+};
+
+// Places of entry base + tid in the list of a key head (0 past the last entry).  All T threads.
+template <int T, bool COOP>
+CSA_DEV int paged_places(const PagedAttnArgs& a, int base, int NB, PagedScratch<T, COOP>& sc)
 {
+    const int tid = threadIdx.x;
+    if (!COOP) return base + tid < NB ? paged_entry<false>(a, base + tid).n + a.item_units : 0;
+    __syncthreads();
+    const int n = min(T, NB - base);
+#pragma unroll 2
+    for (int k = tid >> 5; k < n; k += T / 32) {
+        const int m = paged_entry<true>(a, base + k).n + a.item_units;
+        if ((tid & 31) == 0) sc.places[k] = m;
+    }
+    __syncthreads();
+    return tid < n ? sc.places[tid] : 0;
+}
+
+// T threads call it together.  False: this CTA has no run.
+template <int T, bool COOP>
+CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, COOP>& sc, PagedCursor& c)
+{
+    int64_t* sh = sc.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int NB = a.B * a.n_tiles;
     int64_t sum = 0;
     int n0 = 0;
     for (int base = 0; base < NB; base += T) {
-        const int n = paged_units<COOP>(a, base + tid, NB);
+        const int n = paged_places<T, COOP>(a, base, NB, sc);
         if (base == 0) n0 = n;
         sum += n;
     }
@@ -180,7 +191,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, int64_t* sh, PagedC
     int64_t before = 0;
     for (int base = 0;; base += T) {
         const int e = base + tid;
-        const int n = base == 0 ? n0 : paged_units<COOP>(a, e, NB);
+        const int n = base == 0 ? n0 : paged_places<T, COOP>(a, base, NB, sc);
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

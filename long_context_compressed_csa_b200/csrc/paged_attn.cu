@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 {
     constexpr int R = kSimtRows, U = kSimtUnit, NC = kPagedMaxD / 32;
     extern __shared__ float smem[];
-    __shared__ int64_t sh[kSimtThreads / 32 + 2];
+    __shared__ PagedScratch<kSimtThreads, false> sh;
     __shared__ float sm_m[kSimtWarps][R], sm_l[kSimtWarps][R];
     const int d = a.d, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     float* sq = smem;                      // [R][d]

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
     using S = MmaShape<DP, WR>;
     constexpr int U = S::kU, R = S::kRows, WT = S::kWT, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t sh[kWarps + 2];
+    __shared__ PagedScratch<kThreads, false> sh;
     __shared__ float sm_m[WT * R], sm_l[WT * R];
     __shared__ uint32_t masks[WT * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
     using S = F32Shape<DP, RT>;
     constexpr int U = S::kU, NS = S::kStages, EL = S::kEL, LT = S::kLT, NG = S::kNG, TG = U / NG, ROWB = DP * 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t sh[kWarps + 2];
+    __shared__ PagedScratch<kThreads, false> sh;
     __shared__ float sm_m[kWarps * RT], sm_l[kWarps * RT];
     __shared__ uint32_t masks[kWarps * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;

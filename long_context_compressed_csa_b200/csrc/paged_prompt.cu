@@ -76,6 +76,19 @@ CSA_DEV uint32_t pack2(float x, float y)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Bit i: token j + i is visible to the row (paged_visible), i < 32.
+CSA_DEV uint32_t below32(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+CSA_DEV uint32_t visible32(const RowBounds& r, int j)
+{
+    return below32(r.hi - j) & (~below32(r.lo - j) | below32(r.sink - j));
+}
+// Bits 4 x .. 4 x + 3 of `have`, each for 8 tokens.
+CSA_DEV uint32_t pages32(uint32_t have, int x)
+{
+    const uint32_t h = have >> (4 * x);
+    return (h & 1) * 0xffu | (h >> 1 & 1) * 0xff00u | (h >> 2 & 1) * 0xff0000u | (h >> 3 & 1) * 0xff000000u;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -88,10 +101,10 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sQ = smem;                    // two tiles
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
-    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
+    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
     __shared__ uint32_t have[NS];          // of a V stage: bit i: rows 8 i .. 8 i + 7 have a page
     __shared__ uint32_t tmem_slot;
-    __shared__ int64_t sh[kThreads / 32 + 2];
+    __shared__ PagedScratch<kThreads, true> sh;
     __shared__ volatile int failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     pdl_launch_dependents();
@@ -99,7 +112,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&Qfull[i], kM);
             tc::mbar_init(&Sfull[i], 1);
-            tc::mbar_init(&Pready[i], kM);
+            for (int half = 0; half < 2; ++half) tc::mbar_init(&Pready[i][half], kM);  // of 64 tokens each
             tc::mbar_init(&Ofull[i], 1);
         }
         for (int i = 0; i < NS; ++i) {
@@ -143,32 +156,53 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
         uint32_t n_s = 0, n_q = 0, n_v = 0;  // phases passed: S of this tile, segments of this tile, V tiles
-        bool ok = true;
-        while (ok) {
-            const PagedSegment sg = paged_segment(a, c, cta);
-            if (sg.u0 == sg.u1) break;
+        // A row's part of a segment: loaded while the last product of the segment before runs
+        struct Row {
+            bool tile, in;  // the tile has rows; this is one
+            int64_t at;
+            RowBounds rb;
+        };
+        auto row_of = [&](const PagedEntry& en, int h) {
+            Row x;
+            const int n_rows = paged_rows(a, en.tile);
+            x.tile = w * kM < n_rows;
+            x.in = w * kM + r < n_rows;
+            x.at = x.in ? paged_out_row(a, en.b, en.tile, h, w * kM + r) : 0;
+            x.rb = x.in ? paged_bounds(a, en.b, (en.tile * a.R + w * kM + r) / a.G) : RowBounds{0, 0, 0};
+            return x;
+        };
+        auto load_q = [&](const Row& x, uint4 (&v)[DP / 8]) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + x.at * a.d);
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) v[i] = x.in && i * 8 < a.d ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+        };
+        auto store_q = [&](const uint4 (&v)[DP / 8]) {
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i)
+                *reinterpret_cast<uint4*>(sQ + w * S::kTile + (i >> 3) * (kM * 128) + tc::sw128_offset(r, i & 7)) = v[i];
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&Qfull[w]);
+        };
+        PagedSegment sg = paged_segment(a, c, cta);
+        bool ok = true, more = sg.u0 < sg.u1;
+        Row row;
+        if (more) {
+            row = row_of(c.en, c.h);
+            if (row.tile) {
+                uint4 q[DP / 8];
+                load_q(row, q);
+                store_q(q);
+            }
+        }
+        while (more) {
             if (tid == 0) paged_describe(a, c, sg, cta);
             const PagedEntry en = c.en;
-            const int row = en.tile * a.R + w * kM + r, n_rows = paged_rows(a, en.tile);
-            if (w * kM < n_rows) {
-                const bool in = w * kM + r < n_rows;
-                const int64_t at = in ? paged_out_row(a, en.b, en.tile, c.h, w * kM + r) : 0;
-                const RowBounds rb = in ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
-                {
-                    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at * a.d);
-#pragma unroll
-                    for (int x = 0; x < DP / 8; ++x) {
-                        const uint4 v = in && x * 8 < a.d ? q[x] : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(sQ + w * S::kTile + (x >> 3) * (kM * 128) +
-                                                  tc::sw128_offset(r, x & 7)) = v;
-                    }
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&Qfull[w]);
-                }
-                float* lg = a.logits && in
-                                ? a.logits + (((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap
-                                : nullptr;
-                float m = -INFINITY, l = 0.f;  // m: what the weights in O and l are relative to
+            const int h = c.h;
+            float m = -INFINITY, l = 0.f;  // m: what the weights in O and l are relative to
+            if (row.tile) {
+                float* lg = a.logits && row.in ? a.logits + (((int64_t)en.b * a.n_kv + h) * (a.nq * a.G) +
+                                                             en.tile * a.R + w * kM + r) * a.cap
+                                               : nullptr;
                 for (int u = sg.u0; u < sg.u1 && ok; ++u, ++n_s) {
                     const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
                     ok = all(wait(&Vfull[vs], vt / NS)) && all(wait(&Sfull[w], n_s));
@@ -196,9 +230,12 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);
                     if (!clear) {
 #pragma unroll
-                        for (int i = 0; i < kT; ++i)
-                            if (!((hv >> (i >> 3) & 1) && paged_visible(rb, j0 + i)))
-                                s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t see = visible32(row.rb, j0 + 32 * x) & pages32(hv, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(see >> i & 1)) s[x][i] = __float_as_uint(-INFINITY);
+                        }
                     }
                     if (lg) {
 #pragma unroll
@@ -250,52 +287,67 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                             p[i] = pack2(x.x, x.y);
                         }
                         tmem_st32(s_at + half * 32, p);
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        tc::mbar_arrive(&Pready[w][half]);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(&Pready[w]);
                 }
-                if (ok) ok = all(wait(&Ofull[w], n_q));
-                if (ok) {
-                    tc::fence_after_sync();
-                    const int64_t slot = (int64_t)sg.slot * a.R + w * kM + r;
-                    const float inv = sg.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
-                    for (int x = 0; x < DP; x += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32_async(o_at + x, o);
-                        tc::tmem_wait_ld_regs(o);
-#pragma unroll
-                        for (int y = 0; y < 32; y += 8) {
-                            if (!in || x + y >= a.d) continue;
-                            float v[8];
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[y + z]) * inv;
-                            if (sg.whole && a.out_bf16) {
-                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * a.d + x + y) =
-                                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-                            } else {
-                                float4* to = reinterpret_cast<float4*>(
-                                    sg.whole ? static_cast<float*>(a.out) + at * a.d + x + y : a.part_o + slot * a.d + x + y);
-                                to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                to[1] = make_float4(v[4], v[5], v[6], v[7]);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    if (in) {
-                        if (sg.whole)
-                            paged_store_lse(a, at, en.b, en.tile, c.h, w * kM + r, m, l);
-                        else
-                            a.part_ml[slot] = make_float2(m, l);
-                    }
-                    tc::fence_before_sync();  // these loads, before the next segment's products write O
-                }
-                ++n_q;
             }
             n_v += (uint32_t)(sg.u1 - sg.u0);
-            if (!ok || !paged_next<true>(a, c, sg)) break;
+            const PagedSegment done = sg;
+            const Row out = row;
+            uint4 q[DP / 8];
+            more = ok && paged_next<true>(a, c, sg);
+            if (more) {
+                sg = paged_segment(a, c, cta);
+                more = sg.u0 < sg.u1;
+            }
+            if (more) {
+                row = row_of(c.en, c.h);
+                if (row.tile) load_q(row, q);
+            }
+            if (out.tile && ok) ok = all(wait(&Ofull[w], n_q++));
+            if (!ok) break;
+            // every product of the segment is done: q and S are free
+            if (more && row.tile) store_q(q);
+            if (out.tile) {
+                tc::fence_after_sync();
+                const int64_t slot = (int64_t)done.slot * a.R + w * kM + r;
+                const float inv = done.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+#pragma unroll
+                for (int x = 0; x < DP; x += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32_async(o_at + x, o);
+                    tc::tmem_wait_ld_regs(o);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8) {
+                        if (!out.in || x + y >= a.d) continue;
+                        float v[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[y + z]) * inv;
+                        if (done.whole && a.out_bf16) {
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out.at * a.d + x + y) =
+                                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+                        } else {
+                            float4* to = reinterpret_cast<float4*>(done.whole
+                                                                       ? static_cast<float*>(a.out) + out.at * a.d + x + y
+                                                                       : a.part_o + slot * a.d + x + y);
+                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (out.in) {
+                    if (done.whole)
+                        paged_store_lse(a, out.at, en.b, en.tile, h, w * kM + r, m, l);
+                    else
+                        a.part_ml[slot] = make_float2(m, l);
+                }
+                __syncwarp();
+                tc::fence_before_sync();  // these loads, before the next segment's products write O
+            }
         }
     } else if (some) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -367,9 +419,9 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                                 tc::smem_desc_sw128(k0 + st * S::kTile + at, 16, 1024), kIdescS, x ? 1u : 0u);
             }
         };
-        auto mma_o = [&](int w, uint32_t st, bool more) {
+        auto mma_o = [&](int w, uint32_t st, int half, bool more) {
 #pragma unroll
-            for (int x = 0; x < kT / 16; ++x)
+            for (int x = half * (kT / 32); x < (half + 1) * (kT / 32); ++x)
                 mma_bf16_ts(tO(w), tS(w) + x * 8,
                             tc::smem_desc_sw128(v0 + st * S::kTile + x * 16 * 128, kT * 128, 1024), kIdescO,
                             more || x ? 1u : 0u);
@@ -392,10 +444,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     const uint32_t st = n % NS, nx = (n + 1) % NS;
                     ok = wait(&Vfull[st], n / NS);
                     for (int w = 0; w < tiles && ok; ++w) {
-                        ok = wait(&Pready[w], n_p[w]++);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = wait(&Pready[w][half], n_p[w]);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            mma_o(w, st, half, u > 0);
+                        }
                         if (!ok) break;
-                        tc::fence_after_sync();
-                        mma_o(w, st, u > 0);
+                        ++n_p[w];
                         if (u + 1 < n_u) {
                             if (w == 0) ok = wait(&Kfull[nx], (n + 1) / NS);
                             if (!ok) break;
