@@ -1,7 +1,7 @@
 // paged_attn for many query rows: a prompt, a chunk of one, or a decode step whose query rows fill a tile.
 //
 // Packed rows (query, head of the key head's group) are the M dimension of tcgen05: both products
-//   S = Q K^T (128 rows x 128 tokens)   and   O += P V (128 rows x d)
+//   S = Q K^T (128 rows x 64 tokens)   and   O += P V (128 rows x d)
 // are bf16 tensor-core work with fp32 accumulators in TMEM.  A CTA has two tiles of 128 rows
 // that share every K and V tile, and takes a run of the schedule (paged.cuh):
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread per row: S from TMEM to registers,
@@ -9,10 +9,12 @@
 //                   memory after a segment
 //   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
 //                   not there, or that no row sees, is a box outside the tensor: zeros
-//   warp 9          MMA issue: while one tile's softmax runs, the other tile's products do
-// O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8): S(j) is
-// issued after P(j-1) V, so once S(j) is there O is at rest, and the softmax thread rescales its
-// row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
+//   warp 9          MMA issue
+// A tile has S of two halves of a unit in TMEM: while the softmax has one half, the other's product
+// is done, so the softmax never waits for the tensor cores when these keep up (with one S of 128
+// tokens each tile's softmax and products took turns: 4500 clocks a unit of both tiles).
+// O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8): the softmax
+// thread then waits for the last product with V and rescales its row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
 // operand of the tensor core has to be; the row sum takes the weights before the rounding.
 // The masks (positions, window, first tokens, missing pages) are applied to S only in units that
 // are not wholly visible; there the rows of V that no query sees are set to zero too, since 0 x NaN
@@ -25,10 +27,11 @@ namespace {
 
 constexpr int kM = 128;             // rows of a tile
 constexpr int kT = 128;             // cached tokens of a unit
+constexpr int kH = 64;              // of a half: what one S holds
 constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-// Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
-constexpr int kRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
+// Registers of a thread: launched with 168, then split between the warpgroups (a half row of S, its P and the next q).
+constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
 constexpr float kRescale = 8.0f;    // log2 units
 
@@ -76,6 +79,19 @@ CSA_DEV uint32_t pack2(float x, float y)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// One lane of a converged warp.
+CSA_DEV bool elect()
+{
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
+CSA_DEV float max3(float x, float y, float z)
+{
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
+}
 // Bit i: token j + i is visible to the row (paged_visible), i < 32.
 CSA_DEV uint32_t below32(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 CSA_DEV uint32_t visible32(const RowBounds& r, int j)
@@ -101,7 +117,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sQ = smem;                    // two tiles
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
-    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
+    __shared__ uint64_t Qfull[2], Sfull[2][2], Pready[2][2], Odone[2][2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
     __shared__ uint32_t have[NS];          // of a V stage: bit i: rows 8 i .. 8 i + 7 have a page
     __shared__ uint32_t tmem_slot;
     __shared__ PagedScratch<kThreads, true> sh;
@@ -111,9 +127,13 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&Qfull[i], kM);
-            tc::mbar_init(&Sfull[i], 1);
-            for (int half = 0; half < 2; ++half) tc::mbar_init(&Pready[i][half], kM);  // of 64 tokens each
-            tc::mbar_init(&Ofull[i], 1);
+            for (int half = 0; half < 2; ++half) {
+                tc::mbar_init(&Sfull[i][half], 1);
+                tc::mbar_init(&Pready[i][half], kM);
+                // one for each half: S of a half says that the product two halves before it is done, so
+                // the wait for the last product (by parity) is at most one phase ahead of its barrier
+                tc::mbar_init(&Odone[i][half], 1);
+            }
         }
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&Kfull[i], 1);
@@ -155,7 +175,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
-        uint32_t n_s = 0, n_q = 0, n_v = 0;  // phases passed: S of this tile, segments of this tile, V tiles
+        uint32_t n_s = 0, n_v = 0;  // units of this tile and V tiles begun: the barriers' phases
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
             bool tile, in;  // the tile has rows; this is one
@@ -203,34 +223,35 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 float* lg = a.logits && row.in ? a.logits + (((int64_t)en.b * a.n_kv + h) * (a.nq * a.G) +
                                                              en.tile * a.R + w * kM + r) * a.cap
                                                : nullptr;
-                for (int u = sg.u0; u < sg.u1 && ok; ++u, ++n_s) {
+                for (int g = 2 * sg.u0; g < 2 * sg.u1; ++g) {
+                    const int u = g >> 1, half = g & 1;
                     const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
-                    ok = all(wait(&Vfull[vs], vt / NS)) && all(wait(&Sfull[w], n_s));
+                    const uint32_t sh_at = s_at + half * kH;
+                    ok = all(wait(&Vfull[vs], vt / NS)) && all(wait(&Sfull[w][half], n_s));
                     if (!ok) break;
                     tc::fence_after_sync();
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(s_at + 32 * i, s[i]);
-                    const int j0 = en.first_token(u, kT);
-                    const uint32_t hv = have[vs];
-                    const bool clear = j0 >= en.lo_max && j0 + kT <= en.hi_min && hv == 0xffffu;
+                    const int j0 = en.first_token(u, kT) + half * kH;
+                    const uint32_t hv = have[vs] >> (half * 8) & 0xffu;
+                    const bool clear = j0 >= en.lo_max && j0 + kH <= en.hi_min && hv == 0xffu;
                     if (!clear) {
-                        // rows of V that no query sees: thread r has row r of the tile
-                        const int j = j0 + r;
-                        if (!en.seen(j)) {
+                        // rows of V that no query sees: thread r has row r of the half
+                        if (r < kH && !en.seen(j0 + r)) {
 #pragma unroll
                             for (int x = 0; x < DP / 8; ++x)
                                 *reinterpret_cast<uint4*>(sV + vs * S::kTile + (x >> 3) * (kT * 128) +
-                                                          tc::sw128_offset(r, x & 7)) = make_uint4(0, 0, 0, 0);
+                                                          tc::sw128_offset(half * kH + r, x & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);
+                    uint32_t s[2][32];
+                    tc::tmem_ld32_async(sh_at, s[0]);
+                    tc::tmem_ld32_async(sh_at + 32, s[1]);
+                    tc::tmem_wait_ld_regs(s[0]);  // both have landed; the second names its registers
+                    tc::tmem_wait_ld_regs(s[1]);
                     if (!clear) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
+                        for (int x = 0; x < 2; ++x) {
                             const uint32_t see = visible32(row.rb, j0 + 32 * x) & pages32(hv, x);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -239,26 +260,27 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     }
                     if (lg) {
 #pragma unroll
-                        for (int i = 0; i < kT; ++i)
+                        for (int i = 0; i < kH; ++i)
                             if (j0 + i < a.cap) lg[j0 + i] = __uint_as_float(s[i >> 5][i & 31]) * a.scale_log2;
                     }
                     __syncwarp();
-                    float top = -INFINITY;
-                    {
-                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < kT; i += 4)
+                    for (int i = 0; i < kH; i += 8)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                t4[x] = fmaxf(t4[x], __uint_as_float(s[i >> 5][(i + x) & 31]));
-                        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.scale_log2;
-                    }
+                        for (int x = 0; x < 4; ++x)
+                            t4[x] = max3(t4[x], __uint_as_float(s[i >> 5][(i + 2 * x) & 31]),
+                                         __uint_as_float(s[i >> 5][(i + 2 * x + 1) & 31]));
+                    const float top = max3(t4[0], t4[1], fmaxf(t4[2], t4[3])) * a.scale_log2;
                     const bool grow = top > m + kRescale;  // m = -inf: as soon as anything is visible
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? exp2f(m - top) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (u > sg.u0) {  // before the first product O holds nothing of this segment
+                        if (g > 2 * sg.u0) {  // before the first product O holds nothing of this segment
+                            ok = all(wait(&Odone[w][half ^ 1], half ? n_s : n_s - 1));
+                            if (!ok) break;
+                            tc::fence_after_sync();
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 32) {
                                 uint32_t o[32];
@@ -273,25 +295,22 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     const float neg = m == -INFINITY ? 0.f : -m;
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2), sb = make_float2(neg, neg);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t p[32];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int e = half * 64 + 2 * i;
-                            float2 x = tc::fma2(make_float2(__uint_as_float(s[e >> 5][e & 31]),
-                                                            __uint_as_float(s[e >> 5][(e + 1) & 31])), sc, sb);
-                            x.x = tc::ex2_approx(x.x);
-                            x.y = tc::ex2_approx(x.y);
-                            sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
-                            p[i] = pack2(x.x, x.y);
-                        }
-                        tmem_st32(s_at + half * 32, p);
-                        tc::tmem_wait_st();
-                        tc::fence_before_sync();
-                        tc::mbar_arrive(&Pready[w][half]);
+                    for (int i = 0; i < 32; ++i) {
+                        float2 x = tc::fma2(make_float2(__uint_as_float(s[i >> 4][(2 * i) & 31]),
+                                                        __uint_as_float(s[i >> 4][(2 * i + 1) & 31])), sc, sb);
+                        x.x = tc::ex2_approx(x.x);
+                        x.y = tc::ex2_approx(x.y);
+                        sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
+                        p[i] = pack2(x.x, x.y);
                     }
+                    tmem_st32(sh_at, p);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&Pready[w][half]);
+                    n_s += half;
                 }
             }
             n_v += (uint32_t)(sg.u1 - sg.u0);
@@ -307,7 +326,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 row = row_of(c.en, c.h);
                 if (row.tile) load_q(row, q);
             }
-            if (out.tile && ok) ok = all(wait(&Ofull[w], n_q++));
+            if (out.tile && ok) ok = all(wait(&Odone[w][1], n_s - 1));
             if (!ok) break;
             // every product of the segment is done: q and S are free
             if (more && row.tile) store_q(q);
@@ -405,69 +424,80 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
     } else if (some && warp == kMmaWarp) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
+        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kH, false, false);
         constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kM, DP, false, true);
         uint32_t n = 0;                     // tiles used
-        uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};
+        uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of Pready and Qfull
         bool ok = true;
-        const uint32_t q0 = tc::smem_u32(sQ), k0 = tc::smem_u32(sK), v0 = tc::smem_u32(sV);
-        auto mma_s = [&](int w, uint32_t st) {
+        // The issue is on the path between a tile's P and its next S.  The whole warp runs these loops, so that
+        // descriptors stay in uniform registers, and one lane is elected to issue; a descriptor is one addition:
+        // the low words of the tiles' descriptors (16-byte address units), and their common high words.
+        const uint64_t dk = tc::smem_desc_sw128(0, 16, 1024), dv = tc::smem_desc_sw128(0, kT * 128, 1024);
+        const uint32_t q0 = (uint32_t)dk + (tc::smem_u32(sQ) >> 4), k0 = (uint32_t)dk + (tc::smem_u32(sK) >> 4),
+                       v0 = (uint32_t)dv + (tc::smem_u32(sV) >> 4);
+        const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
+        constexpr uint32_t kStep = S::kTile >> 4;
+        auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+        auto mma_s = [&](int w, uint32_t st, int half) {
+            const uint32_t q = q0 + w * kStep, k = k0 + st * kStep + (half * kH * 128 >> 4);
+            if (elect()) {
 #pragma unroll
-            for (int x = 0; x < DP / 16; ++x) {
-                const uint32_t at = (x >> 2) * (kM * 128) + (x & 3) * 32;
-                tc::mma_bf16_ss(tS(w), tc::smem_desc_sw128(q0 + w * S::kTile + at, 16, 1024),
-                                tc::smem_desc_sw128(k0 + st * S::kTile + at, 16, 1024), kIdescS, x ? 1u : 0u);
+                for (int x = 0; x < DP / 16; ++x) {
+                    const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
+                    tc::mma_bf16_ss(tS(w) + half * kH, desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
+                }
+                tc::mma_commit(&Sfull[w][half]);
             }
+            __syncwarp();
         };
         auto mma_o = [&](int w, uint32_t st, int half, bool more) {
+            const uint32_t v = v0 + st * kStep + (half * kH * 128 >> 4);
+            if (elect()) {
 #pragma unroll
-            for (int x = half * (kT / 32); x < (half + 1) * (kT / 32); ++x)
-                mma_bf16_ts(tO(w), tS(w) + x * 8,
-                            tc::smem_desc_sw128(v0 + st * S::kTile + x * 16 * 128, kT * 128, 1024), kIdescO,
-                            more || x ? 1u : 0u);
+                for (int x = 0; x < kH / 16; ++x)
+                    mma_bf16_ts(tO(w), tS(w) + half * kH + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
+                                more || x ? 1u : 0u);
+                tc::mma_commit(&Odone[w][half]);
+            }
+            __syncwarp();
+        };
+        auto done = [&](uint64_t* bar) {  // arrives when the products issued so far are complete
+            if (elect()) tc::mma_commit(bar);
+            __syncwarp();
         };
         while (ok) {
             const PagedSegment sg = paged_segment(a, c, cta);
             if (sg.u0 == sg.u1) break;
             const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1, n_u = sg.u1 - sg.u0;
-            if (lane == 0) {
-                ok = wait(&Kfull[n % NS], n / NS);
-                for (int w = 0; w < tiles && ok; ++w) {
-                    ok = wait(&Qfull[w], n_q[w]++);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    mma_s(w, n % NS);
-                    tc::mma_commit(&Sfull[w]);
-                }
-                if (ok) tc::mma_commit(&Kempty[n % NS]);
-                for (int u = 0; u < n_u && ok; ++u, ++n) {
-                    const uint32_t st = n % NS, nx = (n + 1) % NS;
-                    ok = wait(&Vfull[st], n / NS);
-                    for (int w = 0; w < tiles && ok; ++w) {
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = wait(&Pready[w][half], n_p[w]);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            mma_o(w, st, half, u > 0);
-                        }
-                        if (!ok) break;
-                        ++n_p[w];
-                        if (u + 1 < n_u) {
-                            if (w == 0) ok = wait(&Kfull[nx], (n + 1) / NS);
-                            if (!ok) break;
-                            mma_s(w, nx);
-                            tc::mma_commit(&Sfull[w]);
-                        } else {
-                            tc::mma_commit(&Ofull[w]);
-                        }
-                    }
-                    if (!ok) break;
-                    tc::mma_commit(&Vempty[st]);
-                    if (u + 1 < n_u) tc::mma_commit(&Kempty[nx]);
-                }
+            ok = all(wait(&Kfull[n % NS], n / NS));
+            for (int w = 0; w < tiles && ok; ++w) {
+                ok = all(wait(&Qfull[w], n_q[w]++));
+                if (!ok) break;
+                tc::fence_after_sync();
+                mma_s(w, n % NS, 0);
+                mma_s(w, n % NS, 1);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            n = __shfl_sync(0xffffffffu, n, 0);
+            if (ok) done(&Kempty[n % NS]);
+            for (int u = 0; u < n_u && ok; ++u, ++n) {
+                const uint32_t st = n % NS, nx = (n + 1) % NS;
+                ok = all(wait(&Vfull[st], n / NS));
+                if (ok && u + 1 < n_u) ok = all(wait(&Kfull[nx], (n + 1) / NS));
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || w >= tiles) continue;
+                        ok = all(wait(&Pready[w][half], n_p[w]));
+                        if (!ok) continue;
+                        tc::fence_after_sync();
+                        mma_o(w, st, half, u > 0 || half > 0);
+                        if (u + 1 < n_u) mma_s(w, nx, half);  // over the P that was just used
+                        n_p[w] += half;
+                    }
+                if (!ok) break;
+                done(&Vempty[st]);
+                if (u + 1 < n_u) done(&Kempty[nx]);
+            }
             if (!ok || !paged_next<true>(a, c, sg)) break;
         }
     }
