@@ -118,7 +118,9 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
     __shared__ uint64_t Qfull[2], Sfull[2][2], Pready[2][2], Odone[2][2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
-    __shared__ uint32_t have[NS];          // of a V stage: bit i: rows 8 i .. 8 i + 7 have a page
+    // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S; by the time
+    // of unit n the V stage of n - NS - 1 has been free, so n - 2 NS is long past.
+    __shared__ uint32_t have[2 * NS];
     __shared__ uint32_t tmem_slot;
     __shared__ PagedScratch<kThreads, true> sh;
     __shared__ volatile int failed;
@@ -126,10 +128,10 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     pdl_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&Qfull[i], kM);
+            tc::mbar_init(&Qfull[i], kM / 32);
             for (int half = 0; half < 2; ++half) {
                 tc::mbar_init(&Sfull[i][half], 1);
-                tc::mbar_init(&Pready[i][half], kM);
+                tc::mbar_init(&Pready[i][half], kM / 32);
                 // one for each half: S of a half says that the product two halves before it is done, so
                 // the wait for the last product (by parity) is at most one phase ahead of its barrier
                 tc::mbar_init(&Odone[i][half], 1);
@@ -182,6 +184,11 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             int64_t at;
             RowBounds rb;
         };
+        // one arrival a warp: 32 on one barrier take their turns, about 400 clocks a half unit
+        auto arrive = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar);
+        };
         auto row_of = [&](const PagedEntry& en, int h) {
             Row x;
             const int n_rows = paged_rows(a, en.tile);
@@ -201,7 +208,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             for (int i = 0; i < DP / 8; ++i)
                 *reinterpret_cast<uint4*>(sQ + w * S::kTile + (i >> 3) * (kM * 128) + tc::sw128_offset(r, i & 7)) = v[i];
             tc::fence_proxy_async_smem();
-            tc::mbar_arrive(&Qfull[w]);
+            arrive(&Qfull[w]);
         };
         PagedSegment sg = paged_segment(a, c, cta);
         bool ok = true, more = sg.u0 < sg.u1;
@@ -227,14 +234,16 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     const int u = g >> 1, half = g & 1;
                     const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
                     const uint32_t sh_at = s_at + half * kH;
-                    ok = all(wait(&Vfull[vs], vt / NS)) && all(wait(&Sfull[w][half], n_s));
+                    ok = all(wait(&Sfull[w][half], n_s));
                     if (!ok) break;
                     tc::fence_after_sync();
                     const int j0 = en.first_token(u, kT) + half * kH;
-                    const uint32_t hv = have[vs] >> (half * 8) & 0xffu;
+                    const uint32_t hv = have[vt % (2 * NS)] >> (half * 8) & 0xffu;
                     const bool clear = j0 >= en.lo_max && j0 + kH <= en.hi_min && hv == 0xffu;
                     if (!clear) {
                         // rows of V that no query sees: thread r has row r of the half
+                        ok = all(wait(&Vfull[vs], vt / NS));
+                        if (!ok) break;
                         if (r < kH && !en.seen(j0 + r)) {
 #pragma unroll
                             for (int x = 0; x < DP / 8; ++x)
@@ -309,7 +318,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
-                    tc::mbar_arrive(&Pready[w][half]);
+                    arrive(&Pready[w][half]);
                     n_s += half;
                 }
             }
@@ -401,7 +410,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     ok = all(wait(empty, ph));
                     if (!ok) break;
                     if (lane == 0) {
-                        if (kv) have[st] = hv;
+                        if (!kv) have[n % (2 * NS)] = hv;
                         tc::mbar_arrive_expect_tx(full, S::kTile);
                     }
                     __syncwarp();
