@@ -1,7 +1,7 @@
 // paged_attn for many query rows: a prompt, a chunk of one, or a decode step whose query rows fill a tile.
 //
 // Packed rows (query, head of the key head's group) are the M dimension of tcgen05: both products
-//   S = Q K^T (128 rows x 64 tokens)   and   O += P V (128 rows x d)
+//   S = Q K^T (128 rows x 128 tokens)   and   O += P V (128 rows x d)
 // are bf16 tensor-core work with fp32 accumulators in TMEM.  A CTA has two tiles of 128 rows
 // that share every K and V tile, and takes a run of the schedule (paged.cuh):
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread per row: S from TMEM to registers,
@@ -10,11 +10,13 @@
 //   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
 //                   not there, or that no row sees, is a box outside the tensor: zeros
 //   warp 9          MMA issue
-// A tile has S of two halves of a unit in TMEM: while the softmax has one half, the other's product
-// is done, so the softmax never waits for the tensor cores when these keep up (with one S of 128
-// tokens each tile's softmax and products took turns: 4500 clocks a unit of both tiles).
-// O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8): the softmax
-// thread then waits for the last product with V and rescales its row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
+// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half, so the first
+// half's product with V starts under the second half's exponentials, and S(j+1) follows P(j) V.
+// (Two S of 64 tokens a tile, so that S(j+1) is there before P(j), measured slower: a product of
+// N = 64 takes as long as one of 128, since the operand q is read from shared memory either way.)
+// O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8).  S(j) is
+// issued after P(j-1) V, so once S(j) is there O is at rest, and the softmax thread rescales its
+// row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
 // operand of the tensor core has to be; the row sum takes the weights before the rounding.
 // The masks (positions, window, first tokens, missing pages) are applied to S only in units that
 // are not wholly visible; there the rows of V that no query sees are set to zero too, since 0 x NaN
@@ -27,11 +29,11 @@ namespace {
 
 constexpr int kM = 128;             // rows of a tile
 constexpr int kT = 128;             // cached tokens of a unit
-constexpr int kH = 64;              // of a half: what one S holds
+constexpr int kH = 64;              // of a half: P is handed over in two
 constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-// Registers of a thread: launched with 168, then split between the warpgroups (a half row of S, its P and the next q).
-constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
+constexpr int kRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
 constexpr float kRescale = 8.0f;    // log2 units
 
@@ -63,6 +65,15 @@ CSA_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+CSA_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 CSA_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int r, int p)
@@ -117,25 +128,22 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sQ = smem;                    // two tiles
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
-    __shared__ uint64_t Qfull[2], Sfull[2][2], Pready[2][2], Odone[2][2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
+    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
     // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S; by the time
     // of unit n the V stage of n - NS - 1 has been free, so n - 2 NS is long past.
     __shared__ uint32_t have[2 * NS];
     __shared__ uint32_t tmem_slot;
     __shared__ PagedScratch<kThreads, true> sh;
+    __shared__ PagedCursor cursors[8];     // of the softmax warps, whose registers hold S
     __shared__ volatile int failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     pdl_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&Qfull[i], kM / 32);
-            for (int half = 0; half < 2; ++half) {
-                tc::mbar_init(&Sfull[i][half], 1);
-                tc::mbar_init(&Pready[i][half], kM / 32);
-                // one for each half: S of a half says that the product two halves before it is done, so
-                // the wait for the last product (by parity) is at most one phase ahead of its barrier
-                tc::mbar_init(&Odone[i][half], 1);
-            }
+            tc::mbar_init(&Sfull[i], 1);
+            for (int half = 0; half < 2; ++half) tc::mbar_init(&Pready[i][half], kM / 32);
+            tc::mbar_init(&Ofull[i], 1);
         }
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&Kfull[i], 1);
@@ -165,9 +173,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const bool some = paged_schedule<kThreads, true>(a, cta, sh, c);
     // false after a timeout; the caller leaves its loops
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (tc::mbar_wait(bar, phase & 1, tc::kWaitBudget)) return true;
-        failed = 1;
-        return false;
+        // no sleep between the polls: a wake-up costs more than the waits of this kernel last
+        const long long t0 = clock64();
+        while (!tc::mbar_try_wait(bar, phase & 1))
+            if (clock64() - t0 > tc::kWaitBudget) {
+                failed = 1;
+                return false;
+            }
+        return true;
     };
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };  // a warp gives up as one
 
@@ -177,7 +190,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
-        uint32_t n_s = 0, n_v = 0;  // units of this tile and V tiles begun: the barriers' phases
+        uint32_t n_s = 0, n_o = 0, n_v = 0;  // units and segments of this tile, V tiles: the barriers' phases
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
             bool tile, in;  // the tile has rows; this is one
@@ -210,11 +223,22 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             tc::fence_proxy_async_smem();
             arrive(&Qfull[w]);
         };
-        PagedSegment sg = paged_segment(a, c, cta);
+        PagedCursor& cur = cursors[warp];
+        if (lane == 0) cur = c;
+        __syncwarp();
+        auto next = [&](const PagedSegment& sg) {
+            PagedCursor x = cur;
+            const bool more = paged_next<true>(a, x, sg);
+            __syncwarp();
+            if (lane == 0) cur = x;
+            __syncwarp();
+            return more;
+        };
+        PagedSegment sg = paged_segment(a, cur, cta);
         bool ok = true, more = sg.u0 < sg.u1;
         Row row;
         if (more) {
-            row = row_of(c.en, c.h);
+            row = row_of(cur.en, cur.h);
             if (row.tile) {
                 uint4 q[DP / 8];
                 load_q(row, q);
@@ -222,45 +246,43 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
         }
         while (more) {
-            if (tid == 0) paged_describe(a, c, sg, cta);
-            const PagedEntry en = c.en;
-            const int h = c.h;
+            if (tid == 0) paged_describe(a, cur, sg, cta);
+            const int b = cur.en.b, tile = cur.en.tile, h = cur.h;
             float m = -INFINITY, l = 0.f;  // m: what the weights in O and l are relative to
             if (row.tile) {
-                float* lg = a.logits && row.in ? a.logits + (((int64_t)en.b * a.n_kv + h) * (a.nq * a.G) +
-                                                             en.tile * a.R + w * kM + r) * a.cap
+                float* lg = a.logits && row.in ? a.logits + (((int64_t)b * a.n_kv + h) * (a.nq * a.G) +
+                                                             tile * a.R + w * kM + r) * a.cap
                                                : nullptr;
-                for (int g = 2 * sg.u0; g < 2 * sg.u1; ++g) {
-                    const int u = g >> 1, half = g & 1;
+                for (int u = sg.u0; u < sg.u1; ++u, ++n_s) {
                     const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
-                    const uint32_t sh_at = s_at + half * kH;
-                    ok = all(wait(&Sfull[w][half], n_s));
+                    ok = all(wait(&Sfull[w], n_s));
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const int j0 = en.first_token(u, kT) + half * kH;
-                    const uint32_t hv = have[vt % (2 * NS)] >> (half * 8) & 0xffu;
-                    const bool clear = j0 >= en.lo_max && j0 + kH <= en.hi_min && hv == 0xffu;
+                    const PagedEntry& en = cur.en;
+                    const int j0 = en.first_token(u, kT);
+                    const uint32_t hv = have[vt % (2 * NS)];
+                    const bool clear = j0 >= en.lo_max && j0 + kT <= en.hi_min && hv == 0xffffu;
                     if (!clear) {
-                        // rows of V that no query sees: thread r has row r of the half
+                        // rows of V that no query sees: thread r has row r
                         ok = all(wait(&Vfull[vs], vt / NS));
                         if (!ok) break;
-                        if (r < kH && !en.seen(j0 + r)) {
+                        if (!en.seen(j0 + r)) {
 #pragma unroll
                             for (int x = 0; x < DP / 8; ++x)
                                 *reinterpret_cast<uint4*>(sV + vs * S::kTile + (x >> 3) * (kT * 128) +
-                                                          tc::sw128_offset(half * kH + r, x & 7)) = make_uint4(0, 0, 0, 0);
+                                                          tc::sw128_offset(r, x & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    uint32_t s[2][32];
-                    tc::tmem_ld32_async(sh_at, s[0]);
-                    tc::tmem_ld32_async(sh_at + 32, s[1]);
-                    tc::tmem_wait_ld_regs(s[0]);  // both have landed; the second names its registers
-                    tc::tmem_wait_ld_regs(s[1]);
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(s_at + 32 * i, s[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);  // all have landed; each names its registers
                     if (!clear) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
+                        for (int x = 0; x < 4; ++x) {
                             const uint32_t see = visible32(row.rb, j0 + 32 * x) & pages32(hv, x);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -269,13 +291,13 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     }
                     if (lg) {
 #pragma unroll
-                        for (int i = 0; i < kH; ++i)
+                        for (int i = 0; i < kT; ++i)
                             if (j0 + i < a.cap) lg[j0 + i] = __uint_as_float(s[i >> 5][i & 31]) * a.scale_log2;
                     }
                     __syncwarp();
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < kH; i += 8)
+                    for (int i = 0; i < kT; i += 8)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             t4[x] = max3(t4[x], __uint_as_float(s[i >> 5][(i + 2 * x) & 31]),
@@ -286,10 +308,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         const float f = grow ? exp2f(m - top) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (g > 2 * sg.u0) {  // before the first product O holds nothing of this segment
-                            ok = all(wait(&Odone[w][half ^ 1], half ? n_s : n_s - 1));
-                            if (!ok) break;
-                            tc::fence_after_sync();
+                        if (u > sg.u0) {  // before the first product O holds nothing of this segment
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 32) {
                                 uint32_t o[32];
@@ -304,38 +323,47 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     const float neg = m == -INFINITY ? 0.f : -m;
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2), sb = make_float2(neg, neg);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t p[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float2 x = tc::fma2(make_float2(__uint_as_float(s[i >> 4][(2 * i) & 31]),
-                                                        __uint_as_float(s[i >> 4][(2 * i + 1) & 31])), sc, sb);
-                        x.x = tc::ex2_approx(x.x);
-                        x.y = tc::ex2_approx(x.y);
-                        sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
-                        p[i] = pack2(x.x, x.y);
+                    for (int quarter = 0; quarter < 4; ++quarter) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = quarter * 32 + 2 * i;
+                            float2 x = tc::fma2(make_float2(__uint_as_float(s[e >> 5][e & 31]),
+                                                            __uint_as_float(s[e >> 5][(e + 1) & 31])), sc, sb);
+                            x.x = tc::ex2_approx(x.x);
+                            x.y = tc::ex2_approx(x.y);
+                            sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
+                            p[i] = pack2(x.x, x.y);
+                        }
+                        // the first half is handed over once the third quarter's exponentials hid its stores
+                        if (quarter == 2) {
+                            tc::tmem_wait_st();
+                            tc::fence_before_sync();
+                            arrive(&Pready[w][0]);
+                        }
+                        tmem_st16(s_at + quarter * 16, p);
                     }
-                    tmem_st32(sh_at, p);
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
-                    arrive(&Pready[w][half]);
-                    n_s += half;
+                    arrive(&Pready[w][1]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
             }
             n_v += (uint32_t)(sg.u1 - sg.u0);
             const PagedSegment done = sg;
             const Row out = row;
             uint4 q[DP / 8];
-            more = ok && paged_next<true>(a, c, sg);
+            more = ok && next(sg);
             if (more) {
-                sg = paged_segment(a, c, cta);
+                sg = paged_segment(a, cur, cta);
                 more = sg.u0 < sg.u1;
             }
             if (more) {
-                row = row_of(c.en, c.h);
+                row = row_of(cur.en, cur.h);
                 if (row.tile) load_q(row, q);
             }
-            if (out.tile && ok) ok = all(wait(&Odone[w][1], n_s - 1));
+            if (out.tile && ok) ok = all(wait(&Ofull[w], n_o++));
             if (!ok) break;
             // every product of the segment is done: q and S are free
             if (more && row.tile) store_q(q);
@@ -369,7 +397,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 }
                 if (out.in) {
                     if (done.whole)
-                        paged_store_lse(a, out.at, en.b, en.tile, h, w * kM + r, m, l);
+                        paged_store_lse(a, out.at, b, tile, h, w * kM + r, m, l);
                     else
                         a.part_ml[slot] = make_float2(m, l);
                 }
@@ -433,7 +461,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
     } else if (some && warp == kMmaWarp) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kH, false, false);
+        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
         constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kM, DP, false, true);
         uint32_t n = 0;                     // tiles used
         uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of Pready and Qfull
@@ -447,26 +475,25 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
         constexpr uint32_t kStep = S::kTile >> 4;
         auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-        auto mma_s = [&](int w, uint32_t st, int half) {
-            const uint32_t q = q0 + w * kStep, k = k0 + st * kStep + (half * kH * 128 >> 4);
+        auto mma_s = [&](int w, uint32_t st) {
+            const uint32_t q = q0 + w * kStep, k = k0 + st * kStep;
             if (elect()) {
 #pragma unroll
                 for (int x = 0; x < DP / 16; ++x) {
                     const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
-                    tc::mma_bf16_ss(tS(w) + half * kH, desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
+                    tc::mma_bf16_ss(tS(w), desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
                 }
-                tc::mma_commit(&Sfull[w][half]);
+                tc::mma_commit(&Sfull[w]);
             }
             __syncwarp();
         };
-        auto mma_o = [&](int w, uint32_t st, int half, bool more) {
-            const uint32_t v = v0 + st * kStep + (half * kH * 128 >> 4);
+        auto mma_o = [&](int w, uint32_t st, int half, bool more, bool last) {
+            const uint32_t v = v0 + st * kStep;
             if (elect()) {
 #pragma unroll
-                for (int x = 0; x < kH / 16; ++x)
-                    mma_bf16_ts(tO(w), tS(w) + half * kH + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
-                                more || x ? 1u : 0u);
-                tc::mma_commit(&Odone[w][half]);
+                for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
+                    mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO, more || x ? 1u : 0u);
+                if (last) tc::mma_commit(&Ofull[w]);
             }
             __syncwarp();
         };
@@ -483,8 +510,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 ok = all(wait(&Qfull[w], n_q[w]++));
                 if (!ok) break;
                 tc::fence_after_sync();
-                mma_s(w, n % NS, 0);
-                mma_s(w, n % NS, 1);
+                mma_s(w, n % NS);
             }
             if (ok) done(&Kempty[n % NS]);
             for (int u = 0; u < n_u && ok; ++u, ++n) {
@@ -492,17 +518,18 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 ok = all(wait(&Vfull[st], n / NS));
                 if (ok && u + 1 < n_u) ok = all(wait(&Kfull[nx], (n + 1) / NS));
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= tiles) continue;
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (!ok || w >= tiles) continue;
-                        ok = all(wait(&Pready[w][half], n_p[w]));
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && all(wait(&Pready[w][half], n_p[w]));
                         if (!ok) continue;
                         tc::fence_after_sync();
-                        mma_o(w, st, half, u > 0 || half > 0);
-                        if (u + 1 < n_u) mma_s(w, nx, half);  // over the P that was just used
-                        n_p[w] += half;
+                        mma_o(w, st, half, u > 0, half == 1 && u + 1 == n_u);
                     }
+                    if (ok && u + 1 < n_u) mma_s(w, nx);  // over the P that was just used
+                    ++n_p[w];
+                }
                 if (!ok) break;
                 done(&Vempty[st]);
                 if (u + 1 < n_u) done(&Kempty[nx]);
