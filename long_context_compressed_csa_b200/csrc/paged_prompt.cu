@@ -174,6 +174,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     // false after a timeout; the caller leaves its loops
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         // no sleep between the polls: a wake-up costs more than the waits of this kernel last
+        if (tc::mbar_try_wait(bar, phase & 1)) return true;
         const long long t0 = clock64();
         while (!tc::mbar_try_wait(bar, phase & 1))
             if (clock64() - t0 > tc::kWaitBudget) {
@@ -475,31 +476,21 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
         constexpr uint32_t kStep = S::kTile >> 4;
         auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+        // by the elected lane
         auto mma_s = [&](int w, uint32_t st) {
             const uint32_t q = q0 + w * kStep, k = k0 + st * kStep;
-            if (elect()) {
 #pragma unroll
-                for (int x = 0; x < DP / 16; ++x) {
-                    const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
-                    tc::mma_bf16_ss(tS(w), desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
-                }
-                tc::mma_commit(&Sfull[w]);
+            for (int x = 0; x < DP / 16; ++x) {
+                const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
+                tc::mma_bf16_ss(tS(w), desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
             }
-            __syncwarp();
+            tc::mma_commit(&Sfull[w]);
         };
-        auto mma_o = [&](int w, uint32_t st, int half, bool more, bool last) {
+        auto mma_o = [&](int w, uint32_t st, int half, bool more) {
             const uint32_t v = v0 + st * kStep;
-            if (elect()) {
 #pragma unroll
-                for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
-                    mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO, more || x ? 1u : 0u);
-                if (last) tc::mma_commit(&Ofull[w]);
-            }
-            __syncwarp();
-        };
-        auto done = [&](uint64_t* bar) {  // arrives when the products issued so far are complete
-            if (elect()) tc::mma_commit(bar);
-            __syncwarp();
+            for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
+                mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO, more || x ? 1u : 0u);
         };
         while (ok) {
             const PagedSegment sg = paged_segment(a, c, cta);
@@ -510,29 +501,42 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 ok = all(wait(&Qfull[w], n_q[w]++));
                 if (!ok) break;
                 tc::fence_after_sync();
-                mma_s(w, n % NS);
+                if (elect()) {
+                    mma_s(w, n % NS);
+                    if (w == tiles - 1) tc::mma_commit(&Kempty[n % NS]);
+                }
+                __syncwarp();
             }
-            if (ok) done(&Kempty[n % NS]);
             for (int u = 0; u < n_u && ok; ++u, ++n) {
                 const uint32_t st = n % NS, nx = (n + 1) % NS;
+                const bool more = u + 1 < n_u;
                 ok = all(wait(&Vfull[st], n / NS));
-                if (ok && u + 1 < n_u) ok = all(wait(&Kfull[nx], (n + 1) / NS));
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    if (w >= tiles) continue;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && all(wait(&Pready[w][half], n_p[w]));
-                        if (!ok) continue;
-                        tc::fence_after_sync();
-                        mma_o(w, st, half, u > 0, half == 1 && u + 1 == n_u);
-                    }
-                    if (ok && u + 1 < n_u) mma_s(w, nx);  // over the P that was just used
+                    if (!ok || w >= tiles) continue;
+                    ok = all(wait(&Pready[w][0], n_p[w]));
+                    if (!ok) continue;
+                    tc::fence_after_sync();
+                    if (elect()) mma_o(w, st, 0, u > 0);
+                    __syncwarp();
+                    if (w == 0 && more) ok = all(wait(&Kfull[nx], (n + 1) / NS));
+                    ok = ok && all(wait(&Pready[w][1], n_p[w]));
+                    if (!ok) continue;
                     ++n_p[w];
+                    tc::fence_after_sync();
+                    if (elect()) {
+                        mma_o(w, st, 1, true);
+                        if (more)
+                            mma_s(w, nx);  // over the P that was just used
+                        else
+                            tc::mma_commit(&Ofull[w]);
+                        if (w == tiles - 1) {
+                            tc::mma_commit(&Vempty[st]);
+                            if (more) tc::mma_commit(&Kempty[nx]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                done(&Vempty[st]);
-                if (u + 1 < n_u) done(&Kempty[nx]);
             }
             if (!ok || !paged_next<true>(a, c, sg)) break;
         }
