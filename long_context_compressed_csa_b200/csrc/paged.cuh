@@ -63,14 +63,17 @@ struct PagedAttnArgs {
 
 // Tokens [0, sink) and [lo, hi) are visible to query i of sequence b, sink <= lo <= hi (empty: hi = 0).
 struct RowBounds { int lo, hi, sink; };
-CSA_DEV RowBounds paged_bounds(const PagedAttnArgs& a, int b, int i)
+CSA_DEV RowBounds paged_bounds_at(const PagedAttnArgs& a, int64_t t)
 {
-    const int64_t t = a.t[(int64_t)b * a.nq + i];
     RowBounds r;
     r.hi = t < 0 ? 0 : (int)min(t + 1, (int64_t)a.cap);
     r.lo = a.n_win > 0 ? (int)min(max(t - a.n_win + 1, (int64_t)0), (int64_t)r.hi) : 0;
     r.sink = min(a.n_sink, r.lo);
     return r;
+}
+CSA_DEV RowBounds paged_bounds(const PagedAttnArgs& a, int b, int i)
+{
+    return paged_bounds_at(a, a.t[(int64_t)b * a.nq + i]);
 }
 CSA_DEV bool paged_visible(const RowBounds& r, int j) { return j < r.hi && (j >= r.lo || j < r.sink); }
 
@@ -85,36 +88,43 @@ struct PagedEntry {
     CSA_DEV bool seen(int j) const { return j < hi_max && (j >= lo_min || j < sink); }
 };
 
-// COOP: the 32 lanes of a warp share the queries of the entry (a tile of many queries); else the
-// calling thread reads them all.
-template <bool COOP>
+// LANES neighbouring lanes of a converged warp share the queries of the entry (a tile of many); 1: the
+// calling thread reads them all.  Bounds rise with t, so an entry's follow from its smallest and
+// largest t.
+template <int LANES>
 CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
 {
     PagedEntry r;
     r.b = e / a.n_tiles;
     r.tile = e - r.b * a.n_tiles;
     const int row0 = r.tile * a.R, row1 = min(row0 + a.R, a.nq * a.G) - 1;
-    const int i1 = row1 / a.G;
-    r.lo_min = INT32_MAX;
-    r.hi_max = r.sink = r.lo_max = 0;
-    r.hi_min = INT32_MAX;
-    for (int i = row0 / a.G + (COOP ? (int)(threadIdx.x & 31) : 0); i <= i1; i += COOP ? 32 : 1) {
-        const RowBounds w = paged_bounds(a, r.b, i);
-        r.lo_max = max(r.lo_max, w.lo);
-        r.hi_min = min(r.hi_min, w.hi);
-        if (w.hi > 0) {
-            r.lo_min = min(r.lo_min, w.lo);
-            r.hi_max = max(r.hi_max, w.hi);
-            r.sink = max(r.sink, w.sink);
+    const int i0 = row0 / a.G, i1 = row1 / a.G;
+    const int64_t* ts = a.t + (int64_t)r.b * a.nq;
+    constexpr int kAhead = LANES > 1 ? 8 : 1;  // loads under way at once
+    int64_t t_min = INT64_MAX, t_max = INT64_MIN, t_seen = INT64_MAX;  // t_seen: the smallest t >= 0
+    for (int i = i0 + (LANES > 1 ? (int)(threadIdx.x & (LANES - 1)) : 0); i <= i1; i += LANES * kAhead) {
+        int64_t t[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) t[k] = ts[min(i + k * LANES, i1)];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            t_min = min(t_min, t[k]);
+            t_max = max(t_max, t[k]);
+            if (t[k] >= 0) t_seen = min(t_seen, t[k]);
         }
     }
-    if (COOP) {
-        r.lo_max = __reduce_max_sync(0xffffffffu, r.lo_max);
-        r.hi_min = __reduce_min_sync(0xffffffffu, r.hi_min);
-        r.lo_min = __reduce_min_sync(0xffffffffu, r.lo_min);
-        r.hi_max = __reduce_max_sync(0xffffffffu, r.hi_max);
-        r.sink = __reduce_max_sync(0xffffffffu, r.sink);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+        t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, o));
+        t_max = max(t_max, __shfl_xor_sync(0xffffffffu, t_max, o));
+        t_seen = min(t_seen, __shfl_xor_sync(0xffffffffu, t_seen, o));
     }
+    const RowBounds first = paged_bounds_at(a, t_min), last = paged_bounds_at(a, t_max);
+    r.lo_max = last.lo;
+    r.hi_min = first.hi;
+    r.lo_min = t_max >= 0 ? paged_bounds_at(a, t_seen).lo : INT32_MAX;
+    r.hi_max = last.hi;
+    r.sink = last.sink;
     r.w0 = r.hi_max > 0 ? r.lo_min / a.unit : 0;
     r.s1 = (r.sink + a.unit - 1) / a.unit;
     if (r.s1 >= r.w0) r.s1 = r.w0 = 0;  // the first tokens reach the window: one range from 0
@@ -139,32 +149,32 @@ struct PagedCursor {
 };
 
 // Shared memory of paged_schedule.
-template <int T, bool COOP>
+template <int T, int LANES>
 struct PagedScratch {
     int64_t sums[T / 32 + 2];
-    int places[COOP ? T : 1];
+    int places[LANES > 1 ? T : 1];
 };
 
 // Places of entry base + tid in the list of a key head (0 past the last entry).  All T threads.
-template <int T, bool COOP>
-CSA_DEV int paged_places(const PagedAttnArgs& a, int base, int NB, PagedScratch<T, COOP>& sc)
+template <int T, int LANES>
+CSA_DEV int paged_places(const PagedAttnArgs& a, int base, int NB, PagedScratch<T, LANES>& sc)
 {
     const int tid = threadIdx.x;
-    if (!COOP) return base + tid < NB ? paged_entry<false>(a, base + tid).n + a.item_units : 0;
+    if (LANES == 1) return base + tid < NB ? paged_entry<1>(a, base + tid).n + a.item_units : 0;
     __syncthreads();
     const int n = min(T, NB - base);
-#pragma unroll 2
-    for (int k = tid >> 5; k < n; k += T / 32) {
-        const int m = paged_entry<true>(a, base + k).n + a.item_units;
-        if ((tid & 31) == 0) sc.places[k] = m;
+    for (int k0 = 0; k0 < n; k0 += T / LANES) {  // whole warps: the last ones repeat the last entry
+        const int k = k0 + tid / LANES;
+        const int m = paged_entry<LANES>(a, base + min(k, n - 1)).n + a.item_units;
+        if (k < n && tid % LANES == 0) sc.places[k] = m;
     }
     __syncthreads();
     return tid < n ? sc.places[tid] : 0;
 }
 
 // T threads call it together.  False: this CTA has no run.
-template <int T, bool COOP>
-CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, COOP>& sc, PagedCursor& c)
+template <int T, int LANES>
+CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, LANES>& sc, PagedCursor& c)
 {
     int64_t* sh = sc.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -172,7 +182,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, COO
     int64_t sum = 0;
     int n0 = 0;
     for (int base = 0; base < NB; base += T) {
-        const int n = paged_places<T, COOP>(a, base, NB, sc);
+        const int n = paged_places<T, LANES>(a, base, NB, sc);
         if (base == 0) n0 = n;
         sum += n;
     }
@@ -191,7 +201,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, COO
     int64_t before = 0;
     for (int base = 0;; base += T) {
         const int e = base + tid;
-        const int n = base == 0 ? n0 : paged_places<T, COOP>(a, base, NB, sc);
+        const int n = base == 0 ? n0 : paged_places<T, LANES>(a, base, NB, sc);
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -219,7 +229,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, COO
     }
     c.e = (int)sh[T / 32];
     const int64_t off = c.at - sh[T / 32 + 1] * a.n_kv;
-    c.en = paged_entry<COOP>(a, c.e);
+    c.en = paged_entry<(LANES > 1 ? 32 : 1)>(a, c.e);
     const int places = c.en.n + a.item_units;
     c.h = (int)(off / places);
     c.u = (int)(off - (int64_t)c.h * places);
@@ -254,7 +264,7 @@ CSA_DEV void paged_describe(const PagedAttnArgs& a, const PagedCursor& c, const 
     a.desc[cta] = make_int4(c.e, c.h, (int)(((last + 1) * c.ctas - 1) / c.W), 0);
 }
 // On to the next item; false at the end of the run.
-template <bool COOP>
+template <int LANES>
 CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegment& s)
 {
     c.at += s.places;
@@ -262,7 +272,7 @@ CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegme
     c.u = 0;
     if (++c.h == a.n_kv) {
         c.h = 0;
-        c.en = paged_entry<COOP>(a, ++c.e);
+        c.en = paged_entry<LANES>(a, ++c.e);
     }
     return true;
 }

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 {
     constexpr int R = kSimtRows, U = kSimtUnit, NC = kPagedMaxD / 32;
     extern __shared__ float smem[];
-    __shared__ PagedScratch<kSimtThreads, false> sh;
+    __shared__ PagedScratch<kSimtThreads, 1> sh;
     __shared__ float sm_m[kSimtWarps][R], sm_l[kSimtWarps][R];
     const int d = a.d, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     float* sq = smem;                      // [R][d]
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     PagedCursor c;
-    if (!paged_schedule<kSimtThreads, false>(a, cta, sh, c)) return;
+    if (!paged_schedule<kSimtThreads, 1>(a, cta, sh, c)) return;
     const T* K = static_cast<const T*>(a.K);
     const T* V = static_cast<const T*>(a.V);
     while (true) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
         __syncthreads();
         paged_finish_segment<kSimtThreads, kSimtWarps, R>(a, c, sg, so, d, &sm_m[0][0], &sm_l[0][0]);
         __syncthreads();
-        if (!paged_next<false>(a, c, sg)) break;
+        if (!paged_next<1>(a, c, sg)) break;
     }
 }
 

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
     using S = MmaShape<DP, WR>;
     constexpr int U = S::kU, R = S::kRows, WT = S::kWT, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ PagedScratch<kThreads, false> sh;
+    __shared__ PagedScratch<kThreads, 1> sh;
     __shared__ float sm_m[WT * R], sm_l[WT * R];
     __shared__ uint32_t masks[WT * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     PagedCursor c;
-    if (!paged_schedule<kThreads, false>(a, cta, sh, c)) return;
+    if (!paged_schedule<kThreads, 1>(a, cta, sh, c)) return;
     Ring<ROWB, U, WR> ring;
     ring.base = tc::smem_u32(sring) + group * (NS * ring.kStage);
     ring.masks = masks + group * NS;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
         __syncthreads();
         paged_finish_segment<kThreads, WT, R>(a, c, sg, so, DP + 8, sm_m, sm_l);
         __syncthreads();
-        if (!paged_next<false>(a, c, sg)) break;
+        if (!paged_next<1>(a, c, sg)) break;
     }
 }
 
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
     using S = F32Shape<DP, RT>;
     constexpr int U = S::kU, NS = S::kStages, EL = S::kEL, LT = S::kLT, NG = S::kNG, TG = U / NG, ROWB = DP * 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ PagedScratch<kThreads, false> sh;
+    __shared__ PagedScratch<kThreads, 1> sh;
     __shared__ float sm_m[kWarps * RT], sm_l[kWarps * RT];
     __shared__ uint32_t masks[kWarps * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     PagedCursor c;
-    if (!paged_schedule<kThreads, false>(a, cta, sh, c)) return;
+    if (!paged_schedule<kThreads, 1>(a, cta, sh, c)) return;
     Ring<ROWB, U, 1> ring;
     ring.base = tc::smem_u32(smem) + warp * (NS * ring.kStage);
     ring.masks = masks + warp * NS;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
         __syncthreads();
         paged_finish_segment<kThreads, kWarps, RT>(a, c, sg, so, DP + 4, sm_m, sm_l);
         __syncthreads();
-        if (!paged_next<false>(a, c, sg)) break;
+        if (!paged_next<1>(a, c, sg)) break;
     }
 }
 

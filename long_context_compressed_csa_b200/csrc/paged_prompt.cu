@@ -10,8 +10,8 @@
 //   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
 //                   not there, or that no row sees, is a box outside the tensor: zeros
 //   warp 9          MMA issue
-// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half, so the first
-// half's product with V starts under the second half's exponentials, and S(j+1) follows P(j) V.
+// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half (the second
+// first), so one half's product with V starts under the other's exponentials, and S(j+1) follows P(j) V.
 // (Two S of 64 tokens a tile, so that S(j+1) is there before P(j), measured slower: a product of
 // N = 64 takes as long as one of 128, since the operand q is read from shared memory either way.)
 // O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8).  S(j) is
@@ -30,11 +30,8 @@ namespace {
 constexpr int kM = 128;             // rows of a tile
 constexpr int kT = 128;             // cached tokens of a unit
 constexpr int kH = 64;              // of a half: P is handed over in two
-constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
+constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-// Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
-constexpr int kRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
 constexpr float kRescale = 8.0f;    // log2 units
 
 template <int DP>
@@ -42,7 +39,8 @@ struct PromptShape {
     static constexpr int kPanels = DP / 64;
     static constexpr int kTile = kT * DP * 2;           // bytes of a K or V tile (and of a q tile)
     static constexpr int kStages = DP == 64 ? 4 : 2;
-    static constexpr int kSmem = 1024 + 2 * kTile + 2 * kStages * kTile;
+    static constexpr int kStage = 8 * 32 * 128;         // 128 bytes of an output row for each softmax thread
+    static constexpr int kSmem = 1024 + 2 * kTile + 2 * kStages * kTile + kStage;
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A: two values a 32-bit column), fp32 accumulate.
@@ -128,12 +126,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sQ = smem;                    // two tiles
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
+    uint8_t* sO = sV + NS * S::kTile;      // [8 warps][32 rows][128 bytes]
     __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
     // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S; by the time
     // of unit n the V stage of n - NS - 1 has been free, so n - 2 NS is long past.
     __shared__ uint32_t have[2 * NS];
     __shared__ uint32_t tmem_slot;
-    __shared__ PagedScratch<kThreads, true> sh;
+    // before the first tiles arrive
+    PagedScratch<kThreads, 8>& sh = *reinterpret_cast<PagedScratch<kThreads, 8>*>(sK);
     __shared__ PagedCursor cursors[8];     // of the softmax warps, whose registers hold S
     __shared__ volatile int failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -170,7 +170,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     pdl_wait();
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     PagedCursor c;
-    const bool some = paged_schedule<kThreads, true>(a, cta, sh, c);
+    const bool some = paged_schedule<kThreads, 8>(a, cta, sh, c);
     // false after a timeout; the caller leaves its loops
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         // no sleep between the polls: a wake-up costs more than the waits of this kernel last
@@ -186,11 +186,10 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };  // a warp gives up as one
 
     if (some && warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
+        const uint32_t s_at = tS(w) + quarter, p_at = s_at + kT / 2, o_at = tO(w) + quarter;
         uint32_t n_s = 0, n_o = 0, n_v = 0;  // units and segments of this tile, V tiles: the barriers' phases
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
@@ -212,15 +211,27 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             x.rb = x.in ? paged_bounds(a, en.b, (en.tile * a.R + w * kM + r) / a.G) : RowBounds{0, 0, 0};
             return x;
         };
-        auto load_q = [&](const Row& x, uint4 (&v)[DP / 8]) {
-            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + x.at * a.d);
+        // q of the warp's 32 rows, kC lanes to a row
+        constexpr int kC = DP / 8, kRowsAtOnce = 32 / kC;
+        const int qc = lane % kC, qr = lane / kC;
+        auto load_q = [&](const Row& x) {
+            const char* mine = static_cast<const char*>(a.q) + x.at * a.d * 2;
+            const uint32_t ins = __ballot_sync(0xffffffffu, x.in);
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) v[i] = x.in && i * 8 < a.d ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kC; ++i) {
+                const int rr = i * kRowsAtOnce + qr;
+                const char* from = reinterpret_cast<const char*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), rr));
+                const bool in = (ins >> rr & 1) && qc * 8 < a.d;
+                const uint32_t to = tc::smem_u32(sQ) + w * S::kTile + (qc >> 3) * (kM * 128) +
+                                    tc::sw128_offset((r & ~31) + rr, qc & 7);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + (in ? qc * 16 : 0)),
+                             "r"(in ? 16 : 0)
+                             : "memory");
+            }
         };
-        auto store_q = [&](const uint4 (&v)[DP / 8]) {
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i)
-                *reinterpret_cast<uint4*>(sQ + w * S::kTile + (i >> 3) * (kM * 128) + tc::sw128_offset(r, i & 7)) = v[i];
+        auto give_q = [&] {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_proxy_async_smem();
             arrive(&Qfull[w]);
         };
@@ -228,12 +239,27 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (lane == 0) cur = c;
         __syncwarp();
         auto next = [&](const PagedSegment& sg) {
-            PagedCursor x = cur;
-            const bool more = paged_next<true>(a, x, sg);
+            const int64_t at = cur.at + sg.places;
+            if (at >= cur.end) return false;
+            int h = cur.h + 1;
+            PagedEntry en;
+            const bool other = h == a.n_kv;
+            if (other) {
+                h = 0;
+                en = paged_entry<32>(a, cur.e + 1);
+            }
             __syncwarp();
-            if (lane == 0) cur = x;
+            if (lane == 0) {
+                cur.at = at;
+                cur.u = 0;
+                cur.h = h;
+                if (other) {
+                    ++cur.e;
+                    cur.en = en;
+                }
+            }
             __syncwarp();
-            return more;
+            return true;
         };
         PagedSegment sg = paged_segment(a, cur, cta);
         bool ok = true, more = sg.u0 < sg.u1;
@@ -241,9 +267,8 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (more) {
             row = row_of(cur.en, cur.h);
             if (row.tile) {
-                uint4 q[DP / 8];
-                load_q(row, q);
-                store_q(q);
+                load_q(row);
+                give_q();
             }
         }
         while (more) {
@@ -276,34 +301,51 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    uint32_t s[4][32];
+                    // S by quarters of 32 tokens.  One pass for the maximum keeps the last two in registers (all four are
+                    // more than a thread of ten warps has); the first two are read again under the others'
+                    // exponentials.  P lies over the last two.
+                    uint32_t t0[32], t1[32], k2[32], k3[32];
+                    float top = -INFINITY;
+                    auto ready = [&](uint32_t (&v)[32], int quarter) {
+                        tc::tmem_wait_ld_regs(v);
+                        if (!clear) {
+                            const uint32_t see = visible32(row.rb, j0 + 32 * quarter) & pages32(hv, quarter);
+                            if (__any_sync(0xffffffffu, see != ~0u)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(s_at + 32 * i, s[i]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);  // all have landed; each names its registers
-                    if (!clear) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t see = visible32(row.rb, j0 + 32 * x) & pages32(hv, x);
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(see >> i & 1)) v[i] = __float_as_uint(-INFINITY);
+                            }
+                        }
+                    };
+                    auto scan = [&](const uint32_t (&v)[32], int quarter) {
+                        if (lg) {
+                            const int j = j0 + 32 * quarter;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1)) s[x][i] = __float_as_uint(-INFINITY);
+                                if (j + i < a.cap) lg[j + i] = __uint_as_float(v[i]) * a.scale_log2;
                         }
-                    }
-                    if (lg) {
+                        __syncwarp();
+                        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < kT; ++i)
-                            if (j0 + i < a.cap) lg[j0 + i] = __uint_as_float(s[i >> 5][i & 31]) * a.scale_log2;
-                    }
-                    __syncwarp();
-                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        for (int i = 0; i < 32; i += 4)
 #pragma unroll
-                    for (int i = 0; i < kT; i += 8)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            t4[x] = max3(t4[x], __uint_as_float(s[i >> 5][(i + 2 * x) & 31]),
-                                         __uint_as_float(s[i >> 5][(i + 2 * x + 1) & 31]));
-                    const float top = max3(t4[0], t4[1], fmaxf(t4[2], t4[3])) * a.scale_log2;
+                            for (int x = 0; x < 2; ++x)
+                                t[x] = max3(t[x], __uint_as_float(v[i + 2 * x]), __uint_as_float(v[i + 2 * x + 1]));
+                        top = max3(top, t[0], t[1]);
+                    };
+                    tc::tmem_ld32_async(s_at, t0);
+                    ready(t0, 0);
+                    tc::tmem_ld32_async(s_at + 32, t1);
+                    scan(t0, 0);
+                    ready(t1, 1);
+                    tc::tmem_ld32_async(s_at + 64, k2);
+                    scan(t1, 1);
+                    ready(k2, 2);
+                    tc::tmem_ld32_async(s_at + 96, k3);
+                    scan(k2, 2);
+                    ready(k3, 3);
+                    scan(k3, 3);
+                    top *= a.scale_log2;
                     const bool grow = top > m + kRescale;  // m = -inf: as soon as anything is visible
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? exp2f(m - top) : 1.f;
@@ -312,49 +354,53 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         if (u > sg.u0) {  // before the first product O holds nothing of this segment
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 32) {
-                                uint32_t o[32];
-                                tc::tmem_ld32_async(o_at + x, o);
-                                tc::tmem_wait_ld_regs(o);
+                                tc::tmem_ld32_async(o_at + x, t0);
+                                tc::tmem_wait_ld_regs(t0);
 #pragma unroll
-                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                                tmem_st32(o_at + x, o);
+                                for (int y = 0; y < 32; ++y) t0[y] = __float_as_uint(__uint_as_float(t0[y]) * f);
+                                tmem_st32(o_at + x, t0);
                             }
                         }
                     }
                     const float neg = m == -INFINITY ? 0.f : -m;
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2), sb = make_float2(neg, neg);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int quarter = 0; quarter < 4; ++quarter) {
-                        uint32_t p[16];
+                    uint32_t p[16];
+                    auto weights = [&](const uint32_t (&v)[32]) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int e = quarter * 32 + 2 * i;
-                            float2 x = tc::fma2(make_float2(__uint_as_float(s[e >> 5][e & 31]),
-                                                            __uint_as_float(s[e >> 5][(e + 1) & 31])), sc, sb);
+                            float2 x = tc::fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc, sb);
                             x.x = tc::ex2_approx(x.x);
                             x.y = tc::ex2_approx(x.y);
                             sum[i & 1] = tc::fma2(x, make_float2(1.f, 1.f), sum[i & 1]);
                             p[i] = pack2(x.x, x.y);
                         }
-                        // the first half is handed over once the third quarter's exponentials hid its stores
-                        if (quarter == 2) {
-                            tc::tmem_wait_st();
-                            tc::fence_before_sync();
-                            arrive(&Pready[w][0]);
-                        }
-                        tmem_st16(s_at + quarter * 16, p);
-                    }
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    arrive(&Pready[w][1]);
+                    };
+                    auto hand_over = [&](int half) {
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        arrive(&Pready[w][half]);
+                    };
+                    tc::tmem_ld32_async(s_at, t0);
+                    weights(k2);
+                    tmem_st16(p_at + 32, p);
+                    weights(k3);
+                    tmem_st16(p_at + 48, p);
+                    ready(t0, 0);
+                    tc::tmem_ld32_async(s_at + 32, t1);
+                    weights(t0);
+                    hand_over(1);  // its stores are done by now
+                    tmem_st16(p_at, p);
+                    ready(t1, 1);
+                    weights(t1);
+                    tmem_st16(p_at + 16, p);
+                    hand_over(0);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
             }
             n_v += (uint32_t)(sg.u1 - sg.u0);
             const PagedSegment done = sg;
             const Row out = row;
-            uint4 q[DP / 8];
             more = ok && next(sg);
             if (more) {
                 sg = paged_segment(a, cur, cta);
@@ -362,39 +408,62 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
             if (more) {
                 row = row_of(cur.en, cur.h);
-                if (row.tile) load_q(row, q);
+                // S of the last unit was there: no product reads q any more
+                if (row.tile) load_q(row);
             }
             if (out.tile && ok) ok = all(wait(&Ofull[w], n_o++));
             if (!ok) break;
-            // every product of the segment is done: q and S are free
-            if (more && row.tile) store_q(q);
+            // every product of the segment is done
+            if (more && row.tile) give_q();
             if (out.tile) {
                 tc::fence_after_sync();
                 const int64_t slot = (int64_t)done.slot * a.R + w * kM + r;
                 const float inv = done.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                // through shared memory, so that a warp writes whole lines: 128 bytes of each of its rows at a time,
+                // 16-byte chunks swizzled by the row
+                uint8_t* so = sO + warp * (32 * 128);
+                const bool bf16 = done.whole && a.out_bf16;
+                char* mine = bf16         ? static_cast<char*>(a.out) + out.at * a.d * 2
+                             : done.whole ? static_cast<char*>(a.out) + out.at * a.d * 4
+                                          : reinterpret_cast<char*>(a.part_o + slot * a.d);
+                const uint32_t ins = __ballot_sync(0xffffffffu, out.in);
+                const int row_bytes = a.d * (bf16 ? 2 : 4);
+                auto flush = [&](int byte) {  // 8 lanes to a row
+                    __syncwarp();
+                    const int k = lane & 7, at = byte + k * 16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3);
+                        char* to = reinterpret_cast<char*>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), rr));
+                        if ((ins >> rr & 1) && at < row_bytes)
+                            *reinterpret_cast<uint4*>(to + at) =
+                                *reinterpret_cast<const uint4*>(so + rr * 128 + ((k ^ (rr & 7)) << 4));
+                    }
+                    __syncwarp();
+                };
 #pragma unroll
                 for (int x = 0; x < DP; x += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32_async(o_at + x, o);
                     tc::tmem_wait_ld_regs(o);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        if (!out.in || x + y >= a.d) continue;
-                        float v[8];
+                    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+                    if (bf16) {
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[y + z]) * inv;
-                        if (done.whole && a.out_bf16) {
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out.at * a.d + x + y) =
+                        for (int k = 0; k < 4; ++k) {
+                            const float* v = reinterpret_cast<const float*>(o) + 8 * k;
+                            *reinterpret_cast<uint4*>(so + lane * 128 + (((x / 8 % 8 + k) ^ (lane & 7)) << 4)) =
                                 make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-                        } else {
-                            float4* to = reinterpret_cast<float4*>(done.whole
-                                                                       ? static_cast<float*>(a.out) + out.at * a.d + x + y
-                                                                       : a.part_o + slot * a.d + x + y);
-                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
                         }
+                        if (x % 64 == 32) flush((x - 32) * 2);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4*>(so + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        flush(x * 4);
                     }
-                    __syncwarp();
                 }
                 if (out.in) {
                     if (done.whole)
@@ -407,138 +476,139 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
         }
     } else if (some) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    }
-    if (some && warp == kLoadWarp) {
-        // ------------------------------------------------------------ K and V
-        uint32_t n = 0;  // tiles begun
-        bool ok = true;
-        const int boxes = kT / box_rows, none = (int)a.pl.n_pages;
-        while (ok) {
-            const PagedSegment sg = paged_segment(a, c, cta);
-            if (sg.u0 == sg.u1) break;
-            for (int u = sg.u0; u < sg.u1; ++u, ++n) {
-                const int j = c.en.first_token(u, kT) + lane * box_rows;
-                int page = none, in = 0;
-                const bool any = j < c.en.hi_max && (j < c.en.sink || j + box_rows > c.en.lo_min);
-                if (lane < boxes && any && j < a.cap) {
-                    const int p = j / a.pl.page;
-                    const int id = a.pl.table[(int64_t)c.en.b * a.pl.max_pages + p];
-                    if ((uint32_t)id < (uint32_t)none) {
-                        page = id;
-                        in = j - p * a.pl.page;
-                    }
-                }
-                const unsigned there = __ballot_sync(0xffffffffu, page != none);
-                uint32_t hv = 0;
-                for (int i = 0; i < kT / 8; ++i) hv |= (there >> (i * 8 / box_rows) & 1u) << i;
-                const uint32_t st = n % NS, ph = n / NS + 1;  // waits of the first round pass at once
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    uint64_t *full = kv ? &Vfull[st] : &Kfull[st], *empty = kv ? &Vempty[st] : &Kempty[st];
-                    ok = all(wait(empty, ph));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (!kv) have[n % (2 * NS)] = hv;
-                        tc::mbar_arrive_expect_tx(full, S::kTile);
-                    }
-                    __syncwarp();
-                    if (lane < boxes) {
-                        uint8_t* dst = (kv ? sV : sK) + st * S::kTile + lane * box_rows * 128;
-#pragma unroll
-                        for (int x = 0; x < S::kPanels; ++x)
-                            tma_load_4d(dst + x * (kT * 128), kv ? &map_v : &map_k, full, x * 64, c.h, in, page);
-                    }
-                }
-                if (!ok) break;
-            }
-            if (!ok || !paged_next<true>(a, c, sg)) break;
-        }
-        // no copy is in flight when the CTA ends: on the normal path the products have waited for them
-        if (!ok)
-            for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k) {
-                wait(&Kfull[k % NS], k / NS);
-                wait(&Vfull[k % NS], k / NS);
-            }
-    } else if (some && warp == kMmaWarp) {
-        // ------------------------------------------------------------ products
-        constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
-        constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kM, DP, false, true);
-        uint32_t n = 0;                     // tiles used
-        uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of Pready and Qfull
-        bool ok = true;
-        // The issue is on the path between a tile's P and its next S.  The whole warp runs these loops, so that
-        // descriptors stay in uniform registers, and one lane is elected to issue; a descriptor is one addition:
-        // the low words of the tiles' descriptors (16-byte address units), and their common high words.
-        const uint64_t dk = tc::smem_desc_sw128(0, 16, 1024), dv = tc::smem_desc_sw128(0, kT * 128, 1024);
-        const uint32_t q0 = (uint32_t)dk + (tc::smem_u32(sQ) >> 4), k0 = (uint32_t)dk + (tc::smem_u32(sK) >> 4),
-                       v0 = (uint32_t)dv + (tc::smem_u32(sV) >> 4);
-        const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
-        constexpr uint32_t kStep = S::kTile >> 4;
-        auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-        // by the elected lane
-        auto mma_s = [&](int w, uint32_t st) {
-            const uint32_t q = q0 + w * kStep, k = k0 + st * kStep;
-#pragma unroll
-            for (int x = 0; x < DP / 16; ++x) {
-                const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
-                tc::mma_bf16_ss(tS(w), desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
-            }
-            tc::mma_commit(&Sfull[w]);
-        };
-        auto mma_o = [&](int w, uint32_t st, int half, bool more) {
-            const uint32_t v = v0 + st * kStep;
-#pragma unroll
-            for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
-                mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO, more || x ? 1u : 0u);
-        };
-        while (ok) {
-            const PagedSegment sg = paged_segment(a, c, cta);
-            if (sg.u0 == sg.u1) break;
-            const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1, n_u = sg.u1 - sg.u0;
-            ok = all(wait(&Kfull[n % NS], n / NS));
-            for (int w = 0; w < tiles && ok; ++w) {
-                ok = all(wait(&Qfull[w], n_q[w]++));
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (elect()) {
-                    mma_s(w, n % NS);
-                    if (w == tiles - 1) tc::mma_commit(&Kempty[n % NS]);
-                }
-                __syncwarp();
-            }
-            for (int u = 0; u < n_u && ok; ++u, ++n) {
-                const uint32_t st = n % NS, nx = (n + 1) % NS;
-                const bool more = u + 1 < n_u;
-                ok = all(wait(&Vfull[st], n / NS));
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (!ok || w >= tiles) continue;
-                    ok = all(wait(&Pready[w][0], n_p[w]));
-                    if (!ok) continue;
-                    tc::fence_after_sync();
-                    if (elect()) mma_o(w, st, 0, u > 0);
-                    __syncwarp();
-                    if (w == 0 && more) ok = all(wait(&Kfull[nx], (n + 1) / NS));
-                    ok = ok && all(wait(&Pready[w][1], n_p[w]));
-                    if (!ok) continue;
-                    ++n_p[w];
-                    tc::fence_after_sync();
-                    if (elect()) {
-                        mma_o(w, st, 1, true);
-                        if (more)
-                            mma_s(w, nx);  // over the P that was just used
-                        else
-                            tc::mma_commit(&Ofull[w]);
-                        if (w == tiles - 1) {
-                            tc::mma_commit(&Vempty[st]);
-                            if (more) tc::mma_commit(&Kempty[nx]);
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ K and V
+            tc::fence_proxy_async_smem();  // the schedule's scratch, before the tiles over it
+            uint32_t n = 0;  // tiles begun
+            bool ok = true;
+            const int boxes = kT / box_rows, none = (int)a.pl.n_pages;
+            while (ok) {
+                const PagedSegment sg = paged_segment(a, c, cta);
+                if (sg.u0 == sg.u1) break;
+                for (int u = sg.u0; u < sg.u1; ++u, ++n) {
+                    const int j = c.en.first_token(u, kT) + lane * box_rows;
+                    int page = none, in = 0;
+                    const bool any = j < c.en.hi_max && (j < c.en.sink || j + box_rows > c.en.lo_min);
+                    if (lane < boxes && any && j < a.cap) {
+                        const int p = j / a.pl.page;
+                        const int id = a.pl.table[(int64_t)c.en.b * a.pl.max_pages + p];
+                        if ((uint32_t)id < (uint32_t)none) {
+                            page = id;
+                            in = j - p * a.pl.page;
                         }
                     }
+                    const unsigned there = __ballot_sync(0xffffffffu, page != none);
+                    uint32_t hv = 0;
+                    for (int i = 0; i < kT / 8; ++i) hv |= (there >> (i * 8 / box_rows) & 1u) << i;
+                    const uint32_t st = n % NS, ph = n / NS + 1;  // waits of the first round pass at once
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        uint64_t *full = kv ? &Vfull[st] : &Kfull[st], *empty = kv ? &Vempty[st] : &Kempty[st];
+                        ok = all(wait(empty, ph));
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (!kv) have[n % (2 * NS)] = hv;
+                            tc::mbar_arrive_expect_tx(full, S::kTile);
+                        }
+                        __syncwarp();
+                        if (lane < boxes) {
+                            uint8_t* dst = (kv ? sV : sK) + st * S::kTile + lane * box_rows * 128;
+#pragma unroll
+                            for (int x = 0; x < S::kPanels; ++x)
+                                tma_load_4d(dst + x * (kT * 128), kv ? &map_v : &map_k, full, x * 64, c.h, in, page);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                if (!ok || !paged_next<32>(a, c, sg)) break;
+            }
+            // no copy is in flight when the CTA ends: on the normal path the products have waited for them
+            if (!ok)
+                for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k) {
+                    wait(&Kfull[k % NS], k / NS);
+                    wait(&Vfull[k % NS], k / NS);
+                }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
+            constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kM, DP, false, true);
+            uint32_t n = 0;                     // tiles used
+            uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of Pready and Qfull
+            bool ok = true;
+            // The issue is on the path between a tile's P and its next S.  The whole warp runs these loops, so that
+            // descriptors stay in uniform registers, and one lane is elected to issue; a descriptor is one addition:
+            // the low words of the tiles' descriptors (16-byte address units), and their common high words.
+            const uint64_t dk = tc::smem_desc_sw128(0, 16, 1024), dv = tc::smem_desc_sw128(0, kT * 128, 1024);
+            const uint32_t q0 = (uint32_t)dk + (tc::smem_u32(sQ) >> 4), k0 = (uint32_t)dk + (tc::smem_u32(sK) >> 4),
+                           v0 = (uint32_t)dv + (tc::smem_u32(sV) >> 4);
+            const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
+            constexpr uint32_t kStep = S::kTile >> 4;
+            auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+            // by the elected lane
+            auto mma_s = [&](int w, uint32_t st) {
+                const uint32_t q = q0 + w * kStep, k = k0 + st * kStep;
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x) {
+                    const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
+                    tc::mma_bf16_ss(tS(w), desc(q + at, dk_hi), desc(k + at, dk_hi), kIdescS, x ? 1u : 0u);
+                }
+                tc::mma_commit(&Sfull[w]);
+            };
+            auto mma_o = [&](int w, uint32_t st, int half, bool more) {
+                const uint32_t v = v0 + st * kStep;
+#pragma unroll
+                for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
+                    mma_bf16_ts(tO(w), tS(w) + kT / 2 + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
+                                more || x > half * (kH / 16) ? 1u : 0u);
+            };
+            while (ok) {
+                const PagedSegment sg = paged_segment(a, c, cta);
+                if (sg.u0 == sg.u1) break;
+                const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1, n_u = sg.u1 - sg.u0;
+                ok = all(wait(&Kfull[n % NS], n / NS));
+                for (int w = 0; w < tiles && ok; ++w) {
+                    ok = all(wait(&Qfull[w], n_q[w]++));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (elect()) {
+                        mma_s(w, n % NS);
+                        if (w == tiles - 1) tc::mma_commit(&Kempty[n % NS]);
+                    }
                     __syncwarp();
                 }
+                for (int u = 0; u < n_u && ok; ++u, ++n) {
+                    const uint32_t st = n % NS, nx = (n + 1) % NS;
+                    const bool more = u + 1 < n_u;
+                    ok = all(wait(&Vfull[st], n / NS));
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || w >= tiles) continue;
+                        ok = all(wait(&Pready[w][1], n_p[w]));
+                        if (!ok) continue;
+                        tc::fence_after_sync();
+                        if (elect()) mma_o(w, st, 1, u > 0);
+                        __syncwarp();
+                        if (w == 0 && more) ok = all(wait(&Kfull[nx], (n + 1) / NS));
+                        ok = ok && all(wait(&Pready[w][0], n_p[w]));
+                        if (!ok) continue;
+                        ++n_p[w];
+                        tc::fence_after_sync();
+                        if (elect()) {
+                            mma_o(w, st, 0, true);
+                            if (more)
+                                mma_s(w, nx);  // over the P that was just used
+                            else
+                                tc::mma_commit(&Ofull[w]);
+                            if (w == tiles - 1) {
+                                tc::mma_commit(&Vempty[st]);
+                                if (more) tc::mma_commit(&Kempty[nx]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!ok || !paged_next<32>(a, c, sg)) break;
             }
-            if (!ok || !paged_next<true>(a, c, sg)) break;
         }
     }
     tc::fence_before_sync();
