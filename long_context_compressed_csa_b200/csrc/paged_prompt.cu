@@ -10,8 +10,8 @@
 //   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
 //                   not there, or that no row sees, is a box outside the tensor: zeros
 //   warp 9          MMA issue
-// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half (the second
-// first), so one half's product with V starts under the other's exponentials, and S(j+1) follows P(j) V.
+// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half, so
+// the first half's product with V starts under the second's exponentials, and S(j+1) follows P(j) V.
 // (Two S of 64 tokens a tile, so that S(j+1) is there before P(j), measured slower: a product of
 // N = 64 takes as long as one of 128, since the operand q is read from shared memory either way.)
 // O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8).  S(j) is
@@ -30,8 +30,11 @@ namespace {
 constexpr int kM = 128;             // rows of a tile
 constexpr int kT = 128;             // cached tokens of a unit
 constexpr int kH = 64;              // of a half: P is handed over in two
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
+constexpr int kRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
 constexpr float kRescale = 8.0f;    // log2 units
 
 template <int DP>
@@ -51,18 +54,6 @@ CSA_DEV void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-CSA_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 CSA_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
@@ -186,10 +177,11 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };  // a warp gives up as one
 
     if (some && warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tS(w) + quarter, p_at = s_at + kT / 2, o_at = tO(w) + quarter;
+        const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
         uint32_t n_s = 0, n_o = 0, n_v = 0;  // units and segments of this tile, V tiles: the barriers' phases
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
@@ -301,50 +293,36 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    // S by quarters of 32 tokens.  One pass for the maximum keeps the last two in registers (all four are
-                    // more than a thread of ten warps has); the first two are read again under the others'
-                    // exponentials.  P lies over the last two.
-                    uint32_t t0[32], t1[32], k2[32], k3[32];
-                    float top = -INFINITY;
-                    auto ready = [&](uint32_t (&v)[32], int quarter) {
-                        tc::tmem_wait_ld_regs(v);
-                        if (!clear) {
-                            const uint32_t see = visible32(row.rb, j0 + 32 * quarter) & pages32(hv, quarter);
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(s_at + 32 * i, s[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::tmem_wait_ld_regs(s[i]);  // all have landed; each names its registers
+                    if (!clear) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t see = visible32(row.rb, j0 + 32 * x) & pages32(hv, x);
                             if (__any_sync(0xffffffffu, see != ~0u)) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (!(see >> i & 1)) v[i] = __float_as_uint(-INFINITY);
+                                    if (!(see >> i & 1)) s[x][i] = __float_as_uint(-INFINITY);
                             }
                         }
-                    };
-                    auto scan = [&](const uint32_t (&v)[32], int quarter) {
-                        if (lg) {
-                            const int j = j0 + 32 * quarter;
+                    }
+                    if (lg) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (j + i < a.cap) lg[j + i] = __uint_as_float(v[i]) * a.scale_log2;
-                        }
-                        __syncwarp();
-                        float t[2] = {-INFINITY, -INFINITY};
+                        for (int i = 0; i < kT; ++i)
+                            if (j0 + i < a.cap) lg[j0 + i] = __uint_as_float(s[i >> 5][i & 31]) * a.scale_log2;
+                    }
+                    __syncwarp();
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                    for (int i = 0; i < kT; i += 8)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                t[x] = max3(t[x], __uint_as_float(v[i + 2 * x]), __uint_as_float(v[i + 2 * x + 1]));
-                        top = max3(top, t[0], t[1]);
-                    };
-                    tc::tmem_ld32_async(s_at, t0);
-                    ready(t0, 0);
-                    tc::tmem_ld32_async(s_at + 32, t1);
-                    scan(t0, 0);
-                    ready(t1, 1);
-                    tc::tmem_ld32_async(s_at + 64, k2);
-                    scan(t1, 1);
-                    ready(k2, 2);
-                    tc::tmem_ld32_async(s_at + 96, k3);
-                    scan(k2, 2);
-                    ready(k3, 3);
-                    scan(k3, 3);
+                        for (int x = 0; x < 4; ++x)
+                            t4[x] = max3(t4[x], __uint_as_float(s[i >> 5][(i + 2 * x) & 31]),
+                                         __uint_as_float(s[i >> 5][(i + 2 * x + 1) & 31]));
+                    float top = max3(t4[0], t4[1], fmaxf(t4[2], t4[3]));
                     top *= a.scale_log2;
                     const bool grow = top > m + kRescale;  // m = -inf: as soon as anything is visible
                     if (__any_sync(0xffffffffu, grow)) {
@@ -354,11 +332,17 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         if (u > sg.u0) {  // before the first product O holds nothing of this segment
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 32) {
-                                tc::tmem_ld32_async(o_at + x, t0);
-                                tc::tmem_wait_ld_regs(t0);
+                                uint32_t o[16], o1[16];
+                                tc::tmem_ld16_async(o_at + x, o);
+                                tc::tmem_ld16_async(o_at + x + 16, o1);
+                                tc::tmem_wait_ld_regs16(o, o1);
 #pragma unroll
-                                for (int y = 0; y < 32; ++y) t0[y] = __float_as_uint(__uint_as_float(t0[y]) * f);
-                                tmem_st32(o_at + x, t0);
+                                for (int y = 0; y < 16; ++y) {
+                                    o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                                    o1[y] = __float_as_uint(__uint_as_float(o1[y]) * f);
+                                }
+                                tmem_st16(o_at + x, o);
+                                tmem_st16(o_at + x + 16, o1);
                             }
                         }
                     }
@@ -381,20 +365,16 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         tc::fence_before_sync();
                         arrive(&Pready[w][half]);
                     };
-                    tc::tmem_ld32_async(s_at, t0);
-                    weights(k2);
-                    tmem_st16(p_at + 32, p);
-                    weights(k3);
-                    tmem_st16(p_at + 48, p);
-                    ready(t0, 0);
-                    tc::tmem_ld32_async(s_at + 32, t1);
-                    weights(t0);
-                    hand_over(1);  // its stores are done by now
-                    tmem_st16(p_at, p);
-                    ready(t1, 1);
-                    weights(t1);
-                    tmem_st16(p_at + 16, p);
-                    hand_over(0);
+                    weights(s[0]);
+                    tmem_st16(s_at, p);
+                    weights(s[1]);
+                    tmem_st16(s_at + 16, p);
+                    weights(s[2]);
+                    hand_over(0);  // its stores were done under the third quarter's exponentials
+                    tmem_st16(s_at + 32, p);
+                    weights(s[3]);
+                    tmem_st16(s_at + 48, p);
+                    hand_over(1);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
             }
@@ -476,6 +456,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
         }
     } else if (some) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ K and V
             tc::fence_proxy_async_smem();  // the schedule's scratch, before the tiles over it
@@ -558,8 +539,8 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 const uint32_t v = v0 + st * kStep;
 #pragma unroll
                 for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
-                    mma_bf16_ts(tO(w), tS(w) + kT / 2 + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
-                                more || x > half * (kH / 16) ? 1u : 0u);
+                    mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
+                                more || x ? 1u : 0u);
             };
             while (ok) {
                 const PagedSegment sg = paged_segment(a, c, cta);
@@ -583,18 +564,18 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         if (!ok || w >= tiles) continue;
-                        ok = all(wait(&Pready[w][1], n_p[w]));
+                        ok = all(wait(&Pready[w][0], n_p[w]));
                         if (!ok) continue;
                         tc::fence_after_sync();
-                        if (elect()) mma_o(w, st, 1, u > 0);
+                        if (elect()) mma_o(w, st, 0, u > 0);
                         __syncwarp();
                         if (w == 0 && more) ok = all(wait(&Kfull[nx], (n + 1) / NS));
-                        ok = ok && all(wait(&Pready[w][0], n_p[w]));
+                        ok = ok && all(wait(&Pready[w][1], n_p[w]));
                         if (!ok) continue;
                         ++n_p[w];
                         tc::fence_after_sync();
                         if (elect()) {
-                            mma_o(w, st, 0, true);
+                            mma_o(w, st, 1, true);
                             if (more)
                                 mma_s(w, nx);  // over the P that was just used
                             else
