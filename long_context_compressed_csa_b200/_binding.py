@@ -66,6 +66,8 @@ class CSAError(RuntimeError):
 def library():
     """Load libcsa_b200.so (raises if it has not been built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -363,24 +365,35 @@ def hca_dense_attn(q, cache, t, m_prime, out, workspace, lse=None, scale=0.0, st
         _stream(stream)))
 
 
-def _here(*ts):
-    """The paged calls launch on the current device; tensors of another one are refused."""
+# The paged calls take a few microseconds on the GPU in a decode step, so their checks are written for time:
+# one comparison for each thing that may differ.
+def _here(stream, *ts):
+    """The paged calls launch on the current device; tensors of another one are refused.  Returns the raw stream."""
     import torch
-    _cuda(*ts)
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for t in ts:
-        if t is not None and t.device.index != torch.cuda.current_device():
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("all tensors must be CUDA tensors")
             raise ValueError("all tensors must be on the current device (cuda:%d)" % torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _pool(K, V, table, B):
     """Strides and sizes of the pools K, V [n_pages, page, n_kv, d] (any page, row and head
     strides, so a permuted [n_pages, n_kv, page, d] pool too) and of the page table [B, max_pages]."""
     import torch
-    assert K.dim() == 4 and V.shape == K.shape and V.stride() == K.stride() and V.dtype == K.dtype
-    assert K.stride(3) == 1 or K.shape[3] == 1
-    assert table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B and table.is_contiguous()
-    n_pages, page, n_kv, d = K.shape
-    return (K.stride(0), K.stride(1), K.stride(2), n_pages, page, _ptr(table), table.shape[1]), n_kv, d
+    shape, strides = K.shape, K.stride()
+    n_pages, page, n_kv, d = shape
+    assert V.shape == shape and V.stride() == strides and V.dtype == K.dtype
+    assert strides[3] == 1 or d == 1
+    rows, max_pages = table.shape
+    assert rows == B and table.dtype == torch.int32 and table.is_contiguous()
+    return (*strides[:3], n_pages, page, table.data_ptr(), max_pages), n_kv, d, page * max_pages
 
 
 def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
@@ -388,15 +401,16 @@ def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
     into the pools [n_pages,page,n_kv,d] at cache positions t int64 [B,nq] (< 0: padding), through
     the page table int32 [B,max_pages]."""
     import torch
-    _here(k, v, K_pages, V_pages, table, t)
-    B, nq = k.shape[:2]
-    pool, n_kv, d = _pool(K_pages, V_pages, table, B)
-    assert k.shape == (B, nq, n_kv, d) and v.shape == k.shape and v.stride() == k.stride()
-    assert k.dtype == v.dtype == K_pages.dtype and (k.stride(3) == 1 or d == 1)
+    raw = _here(stream, k, v, K_pages, V_pages, table, t)
+    shape, strides = k.shape, k.stride()
+    B, nq = shape[:2]
+    pool, n_kv, d, _ = _pool(K_pages, V_pages, table, B)
+    assert shape == (B, nq, n_kv, d) and v.shape == shape and v.stride() == strides
+    assert k.dtype == v.dtype == K_pages.dtype and (strides[3] == 1 or d == 1)
     assert t.dtype == torch.int64 and t.shape == (B, nq) and t.is_contiguous()
     _check("paged_append", library().paged_append(
-        _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), _ptr(K_pages), _ptr(V_pages), *pool, _ptr(t), B, nq,
-        n_kv, d, _dtype(K_pages), _stream(stream)))
+        k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], K_pages.data_ptr(), V_pages.data_ptr(), *pool,
+        t.data_ptr(), B, nq, n_kv, d, _dtype(K_pages), raw))
 
 
 def paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, weights=False) -> int:
@@ -412,10 +426,11 @@ def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.
     acc fp32 [B,n_kv,cap]: acc_out (acc itself if None) = acc + the weight that each cached token
     got, summed over the queries and the query heads of its key head."""
     import torch
-    _here(q, K_pages, V_pages, table, t, out, workspace, lse, acc, acc_out)
-    B, nq, n_h, d = q.shape
-    pool, n_kv, dk = _pool(K_pages, V_pages, table, B)
-    assert dk == d and q.dtype == K_pages.dtype and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
+    raw = _here(stream, q, K_pages, V_pages, table, t, out, workspace, lse, acc, acc_out)
+    shape = q.shape
+    B, nq, n_h, d = shape
+    pool, n_kv, dk, cap = _pool(K_pages, V_pages, table, B)
+    assert dk == d and q.dtype == K_pages.dtype and q.is_contiguous() and out.is_contiguous() and out.shape == shape
     assert t.dtype == torch.int64 and t.shape == (B, nq) and t.is_contiguous()
     assert lse is None or (lse.shape == (B, nq, n_h) and lse.dtype == torch.float32 and lse.is_contiguous())
     if acc is None:
@@ -423,15 +438,12 @@ def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.
     else:
         acc_out = acc if acc_out is None else acc_out
         for x in (acc, acc_out):
-            assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (
-                B, n_kv, table.shape[1] * K_pages.shape[1])
+            assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, cap)
     assert workspace.is_contiguous()
-    _dtype(out)
-    out_bf16 = 1 if out.dtype.itemsize == 2 else 0
     _check("paged_attn", library().paged_attn(
-        _ptr(q), _ptr(K_pages), _ptr(V_pages), *pool, _ptr(t), B, nq, n_h, n_kv, d, int(n_win), int(n_sink),
-        float(scale), _ptr(out), _ptr(lse), _ptr(acc), _ptr(acc_out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _dtype(q), out_bf16, _stream(stream)))
+        q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), *pool, t.data_ptr(), B, nq, n_h, n_kv, d, n_win, n_sink,
+        scale, out.data_ptr(), _at(lse), _at(acc), _at(acc_out), workspace.data_ptr(), workspace.nbytes, _dtype(q),
+        1 if _dtype(out) == CSA_BF16 else 0, raw))
 
 
 def paged_evict(K_pages, V_pages, table, lens, acc, keep, new_table, new_lens, new_acc, idx_out, n_sink=0, n_recent=0,
@@ -441,18 +453,17 @@ def paged_evict(K_pages, V_pages, table, lens, acc, keep, new_table, new_lens, n
     the pages of new_table int32 [B,new_max_pages] (none of them in table).  Writes new_lens int64
     [B], new_acc fp32 [B,n_kv,new_cap] and the old positions idx_out int32 [B,n_kv,keep] (-1 = none)."""
     import torch
-    _here(K_pages, V_pages, table, lens, acc, new_table, new_lens, new_acc, idx_out)
+    raw = _here(stream, K_pages, V_pages, table, lens, acc, new_table, new_lens, new_acc, idx_out)
     B = table.shape[0]
-    pool, n_kv, d = _pool(K_pages, V_pages, table, B)
-    page = K_pages.shape[1]
-    assert new_table.dtype == torch.int32 and new_table.dim() == 2 and new_table.shape[0] == B
-    assert new_table.is_contiguous()
+    pool, n_kv, d, cap = _pool(K_pages, V_pages, table, B)
+    rows, new_pages = new_table.shape
+    assert rows == B and new_table.dtype == torch.int32 and new_table.is_contiguous()
     for x in (lens, new_lens):
         assert x.dtype == torch.int64 and x.shape == (B,) and x.is_contiguous()
-    for x, tab in ((acc, table), (new_acc, new_table)):
-        assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, tab.shape[1] * page)
+    for x, size in ((acc, cap), (new_acc, new_pages * pool[4])):
+        assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, size)
     assert idx_out.dtype == torch.int32 and idx_out.shape == (B, n_kv, keep) and idx_out.is_contiguous()
     _check("paged_evict", library().paged_evict(
-        _ptr(K_pages), _ptr(V_pages), *pool, _ptr(lens), _ptr(acc), B, n_kv, d, int(keep), int(n_sink),
-        int(n_recent), _ptr(new_table), new_table.shape[1], _ptr(new_lens), _ptr(new_acc), _ptr(idx_out),
-        _dtype(K_pages), _stream(stream)))
+        K_pages.data_ptr(), V_pages.data_ptr(), *pool, lens.data_ptr(), acc.data_ptr(), B, n_kv, d, keep, n_sink,
+        n_recent, new_table.data_ptr(), new_pages, new_lens.data_ptr(), new_acc.data_ptr(), idx_out.data_ptr(),
+        _dtype(K_pages), raw))
