@@ -6,7 +6,6 @@
 namespace csa {
 
 constexpr int kPagedMaxD = 256;    // widest head the kernels hold on chip
-constexpr int kPagedMaxCtas = 512; // CTAs of one attention launch (the workspace has two slots for each)
 
 // Pools of K and V rows: row (p, r, h) of d elements starts p * ld_page + r * ld_row + h * ld_head
 // elements after the base; K and V have the same strides.
@@ -46,13 +45,15 @@ struct PagedAttnArgs {
     int unit;              // cached tokens of a schedule unit
     int min_units;         // units a CTA takes at least
     int item_units;        // what an item costs beside its units, in units
-    int grid;              // CTAs launched
+    int runs;              // runs of the schedule
+    int heads;             // lists of runs: worker w has run w / heads (prompt and CUDA-core kernels: one list, a worker
+                           // is a CTA; decode kernels: a list for each key head, a worker is a group of warps)
     // workspace
     uint32_t* status;      // 1 after a timeout
-    int4* desc;            // [grid]: the split item that begins in this CTA {entry, head, last CTA, 1 after a timeout},
-                           // entry -1: none
-    float* part_o;         // [2 * grid][R][d] unnormalised partial outputs
-    float2* part_ml;       // [2 * grid][R] their (running maximum, sum), base 2
+    int4* desc;            // [workers]: the split item that begins in this worker's run {entry, head, runs that have a
+                           // part of it, 1 after a timeout}, entry -1: none
+    float* part_o;         // [2 * workers][R][d] unnormalised partial outputs
+    float2* part_ml;       // [2 * workers][R] their (running maximum, sum), base 2
     // accumulated weights: scaled base-2 logits [B][n_kv][nq * G][cap] and the final base-2
     // log-sum-exp [B][n_kv][nq * G], both in the workspace; null: none asked for
     float* logits;
@@ -134,16 +135,17 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
 }
 
 // The schedule.  The units of all items, in the order (entry, key head, unit), are one list
-// that is cut into equal runs, one for each CTA, whatever the sequences' lengths: a ragged
-// batch and one long sequence both fill the GPU.  An item begins with item_units places
-// that hold no unit: what it costs to begin and end one, so that a run of many short items (the first
-// rows of a prompt) is no longer than one of few long ones.  Only the first and the last item of a run
-// can be cut, so a CTA writes at most two partial results; paged_attn_combine joins them in
-// the order of the CTAs.  The lengths are read on the device, so a captured graph follows them.
+// that is cut into equal runs, whatever the sequences' lengths: a ragged batch and one long sequence both
+// fill the GPU.  (Decode kernels have a list (entry, unit) of each key head, cut alike, so that the heads of a
+// token, which lie together in a [row][head] page, are read at about one time.)  An item begins with
+// item_units places that hold no unit: what it costs to begin and end one, so that a run of many short items
+// (the first rows of a prompt) is no longer than one of few long ones.  Only the first and the last item of a
+// run can be cut, so a run writes at most two partial results; paged_attn_combine joins them in
+// the order of the runs.  The lengths are read on the device, so a captured graph follows them.
 struct PagedCursor {
-    int64_t at, end;       // this CTA's run of the list
+    int64_t at, end;       // this run of the list
     int64_t W;
-    int ctas;              // CTAs that have a run
+    int runs;              // that are not empty
     int e, h, u;           // entry, key head and place within the item of `at`
     PagedEntry en;
 };
@@ -151,7 +153,8 @@ struct PagedCursor {
 // Shared memory of paged_schedule.
 template <int T, int LANES>
 struct PagedScratch {
-    int64_t sums[T / 32 + 2];
+    int64_t sums[T / 32];
+    int64_t upto[T];
     int places[LANES > 1 ? T : 1];
 };
 
@@ -172,13 +175,13 @@ CSA_DEV int paged_places(const PagedAttnArgs& a, int base, int NB, PagedScratch<
     return tid < n ? sc.places[tid] : 0;
 }
 
-// T threads call it together.  False: this CTA has no run.
-template <int T, int LANES>
-CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, LANES>& sc, PagedCursor& c)
+// T threads call it together, each with the run of its warp (PER_WARP) or of the CTA.  False: that run is empty.
+template <int T, int LANES, bool PER_WARP>
+CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int run, PagedScratch<T, LANES>& sc, PagedCursor& c)
 {
     int64_t* sh = sc.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int NB = a.B * a.n_tiles;
+    const int NB = a.B * a.n_tiles, H = PER_WARP ? 1 : a.n_kv;  // heads in a list
     int64_t sum = 0;
     int n0 = 0;
     for (int base = 0; base < NB; base += T) {
@@ -193,14 +196,15 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, LAN
     int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < T / 32; ++w) total += sh[w];
-    c.W = total * a.n_kv;
-    c.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, c.W / a.min_units));
-    if (cta >= c.ctas) return false;
-    c.at = cta * c.W / c.ctas;
-    c.end = (cta + 1) * c.W / c.ctas;
-    int64_t before = 0;
-    for (int base = 0;; base += T) {
-        const int e = base + tid;
+    c.W = total * H;
+    c.runs = (int)max((int64_t)1, min((int64_t)a.runs, c.W / a.min_units));
+    const bool some = run < c.runs;
+    if (!PER_WARP && !some) return false;
+    c.at = run * c.W / c.runs;
+    c.end = (run + 1) * c.W / c.runs;
+    int64_t before = 0, start = 0;  // places (of one key head) before the block of T entries, and before entry c.e
+    c.e = -1;
+    for (int base = 0; base < NB; base += T) {
         const int n = base == 0 ? n0 : paged_places<T, LANES>(a, base, NB, sc);
         int64_t inc = n;
 #pragma unroll
@@ -210,41 +214,38 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int cta, PagedScratch<T, LAN
         }
         __syncthreads();
         if (lane == 31) sh[warp] = inc;
-        if (tid == 0) sh[T / 32] = -1;
+        sc.upto[tid] = inc;  // places of the warp's entries up to and with this one
         __syncthreads();
-        int64_t all = before;
-#pragma unroll
-        for (int w = 0; w < T / 32; ++w) {
-            if (w == warp) inc += all;
-            all += sh[w];
+        for (int w = 0; w < T / 32 && c.e < 0; ++w) {
+            // each warp looks for its own run's start
+            if (c.at < (before + sh[w]) * H) {
+                const int64_t to = before + sc.upto[w * 32 + lane];
+                const int k = __ffs(__ballot_sync(0xffffffffu, c.at < to * H)) - 1;
+                c.e = base + w * 32 + k;
+                start = k > 0 ? __shfl_sync(0xffffffffu, to, k - 1) : before;
+            }
+            before += sh[w];
         }
-        // inc: places (of one key head) up to and with entry e
-        if (n > 0 && (inc - n) * a.n_kv <= c.at && c.at < inc * a.n_kv) {
-            sh[T / 32] = e;
-            sh[T / 32 + 1] = inc - n;
-        }
-        __syncthreads();
-        if (sh[T / 32] >= 0) break;
-        before = all;
+        if (!PER_WARP && c.e >= 0) break;  // alike in all threads; else every warp stays to the end
     }
-    c.e = (int)sh[T / 32];
-    const int64_t off = c.at - sh[T / 32 + 1] * a.n_kv;
+    __syncthreads();  // sc may be reused
+    if (!some) return false;
+    const int64_t off = c.at - start * H;
     c.en = paged_entry<(LANES > 1 ? 32 : 1)>(a, c.e);
     const int places = c.en.n + a.item_units;
     c.h = (int)(off / places);
     c.u = (int)(off - (int64_t)c.h * places);
-    __syncthreads();  // sh may be reused
     return true;
 }
 
-// The part of the current item that this CTA has, and where its result goes.
+// The part of the current item that this run has, and where its result goes.
 struct PagedSegment {
     int places;
     int u0, u1;  // units; empty where the run ends before the item's first unit
     bool whole;
     int slot;    // of a partial result
 };
-CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c, int cta)
+CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c, int worker)
 {
     PagedSegment s;
     const int all = c.en.n + a.item_units, p1 = (int)min((int64_t)all, c.u + (c.end - c.at));
@@ -252,26 +253,26 @@ CSA_DEV PagedSegment paged_segment(const PagedAttnArgs& a, const PagedCursor& c,
     s.u0 = max(0, c.u - a.item_units);
     s.u1 = max(0, p1 - a.item_units);
     s.whole = s.u0 == 0 && s.u1 == c.en.n;
-    s.slot = 2 * cta + (s.u0 == 0 ? 1 : 0);
+    s.slot = 2 * worker + (s.u0 == 0 ? 1 : 0);
     return s;
 }
-// The combine's description of an item whose first units, but not its last, are this CTA's.  One thread.
-CSA_DEV void paged_describe(const PagedAttnArgs& a, const PagedCursor& c, const PagedSegment& s, int cta)
+// The combine's description of an item whose first units, but not its last, are this worker's.  One thread.
+CSA_DEV void paged_describe(const PagedAttnArgs& a, const PagedCursor& c, const PagedSegment& s, int worker)
 {
     if (s.whole || s.u0 > 0 || s.u1 == 0) return;
-    // the run that has the item's last unit: place x lies in run ((x + 1) ctas - 1) / W
+    // the run that has the item's last unit: place x lies in run ((x + 1) runs - 1) / W
     const int64_t last = c.at - c.u + c.en.n + a.item_units - 1;
-    a.desc[cta] = make_int4(c.e, c.h, (int)(((last + 1) * c.ctas - 1) / c.W), 0);
+    a.desc[worker] = make_int4(c.e, c.h, (int)(((last + 1) * c.runs - 1) / c.W) - worker / a.heads + 1, 0);
 }
-// On to the next item; false at the end of the run.
-template <int LANES>
+// On to the next item; false at the end of the run.  PER_WARP: of the same key head.
+template <int LANES, bool PER_WARP>
 CSA_DEV bool paged_next(const PagedAttnArgs& a, PagedCursor& c, const PagedSegment& s)
 {
     c.at += s.places;
     if (c.at >= c.end) return false;
     c.u = 0;
-    if (++c.h == a.n_kv) {
-        c.h = 0;
+    if (PER_WARP || ++c.h == a.n_kv) {
+        if (!PER_WARP) c.h = 0;
         c.en = paged_entry<LANES>(a, ++c.e);
     }
     return true;
@@ -344,8 +345,17 @@ struct PagedShape {
     PagedKind kind;
     int DP;         // head width rounded up to a kernel's
     int WR;         // kPagedMma: row groups of 16; kPagedF32: rows
-    int R, unit, min_units, item_units, grid;
+    int R, unit, min_units, item_units;
+    int workers;    // of a full GPU
+    bool by_head;   // a list of runs for each key head
 };
+// Runs of each of `lists` lists: what fills the GPU, and no more than the capacity has use for.
+inline int paged_runs(const PagedShape& s, int64_t lists, int64_t places)
+{
+    int64_t n = s.workers / lists;
+    if (places / s.min_units < n) n = places / s.min_units;
+    return n < 1 ? 1 : (int)n;
+}
 PagedShape paged_decode_shape(int dtype, int rows, int d);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream);
 

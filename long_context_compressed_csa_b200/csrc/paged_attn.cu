@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     PagedCursor c;
-    if (!paged_schedule<kSimtThreads, 1>(a, cta, sh, c)) return;
+    if (!paged_schedule<kSimtThreads, 1, false>(a, cta, sh, c)) return;
     const T* K = static_cast<const T*>(a.K);
     const T* V = static_cast<const T*>(a.V);
     while (true) {
@@ -136,106 +136,176 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
         __syncthreads();
         paged_finish_segment<kSimtThreads, kSimtWarps, R>(a, c, sg, so, d, &sm_m[0][0], &sm_l[0][0]);
         __syncthreads();
-        if (!paged_next<1>(a, c, sg)) break;
+        if (!paged_next<1, false>(a, c, sg)) break;
     }
 }
 
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-// Joins the partial results of the CTAs that had a part of an item: PS warps of a CTA share the pieces
-// of a row.  A decode call may cut an item into many pieces and has few rows (PS = 4); a prompt's
-// items are cut in two or three and have many (PS = 1).
-template <int PS>
+// Pieces p0, p0 + step, ... of a row: their weighted sum, four under way at once.  slot(p): where piece p lies.
+template <int NC, typename F>
+CSA_DEV void join_pieces(const PagedAttnArgs& a, F slot, int p0, int step, int np, float M, float& L, float (&acc)[NC])
+{
+    constexpr int kAhead = 4;
+    const int lane = threadIdx.x & 31;
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+    for (; p0 < np; p0 += step * kAhead) {
+        float2 ml[kAhead];
+        float v[kAhead][NC];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = slot(min(p0 + k * step, np - 1));
+            ml[k] = a.part_ml[at];
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (lane + 32 * i < a.d) v[k][i] = a.part_o[at * a.d + lane + 32 * i];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float w = p0 + k * step >= np || ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+            if (w == 0.f) continue;
+            L = fmaf(w, ml[k].y, L);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (lane + 32 * i < a.d) acc[i] = fmaf(w, v[k][i], acc[i]);
+        }
+    }
+}
+
+// Joins the partial results of the runs that had a part of an item.  A CTA looks at 32 descriptions together (most
+// workers describe none).  An item of few pieces has a warp for each row; one of many (a long sequence of a
+// small batch) the whole CTA.  NC: columns of a lane.
+template <int NC>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs a)
 {
-    constexpr int NC = kPagedMaxD / 32, RW = kJoinWarps / PS;
-    __shared__ float sh[kJoinWarps][2];
-    __shared__ float so[PS > 1 ? kJoinWarps : 1][kPagedMaxD];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c0 = blockIdx.x;
-    const int r = blockIdx.y * RW + warp / PS, ps = warp % PS;
+    constexpr int kMany = 16;  // pieces that a warp takes by itself: four rounds
+    __shared__ float sh[kJoinWarps];
+    __shared__ float so[kJoinWarps][NC * 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, workers = a.runs * a.heads;
     pdl_launch_dependents();
     pdl_wait();
-    if (c0 == 0 && blockIdx.y == 0 && warp == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
         int late = 0;
-        for (int i = lane; i < a.grid; i += 32) late |= a.desc[i].w;
+        for (int i = lane; i < workers; i += 32) late |= a.desc[i].w;
         late = __any_sync(0xffffffffu, late);
         if (lane == 0) *a.status = late ? 1u : 0u;
     }
-    const int4 ds = a.desc[c0];
-    if (ds.x < 0) return;
-    const int b = ds.x / a.n_tiles, tile = ds.x - b * a.n_tiles, h = ds.y;
-    const int np = ds.z - c0 + 1;
-    const bool in = r < paged_rows(a, tile);
-    // piece p lies in slot 2 c0 + 1 for p = 0, 2 (c0 + p) after that
-    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * a.R + r; };
-    float M = -INFINITY, L = 0.f, acc[NC];
-    if (in)
-        for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
+    for (int base = blockIdx.x; base < workers; base += 32 * gridDim.x) {
+        const int mine = base + lane * gridDim.x;
+        const int4 ds = mine < workers ? a.desc[mine] : make_int4(-1, 0, 0, 0);
+        const unsigned many = __ballot_sync(0xffffffffu, ds.x >= 0 && ds.z > kMany);
+        const unsigned few = __ballot_sync(0xffffffffu, ds.x >= 0 && ds.z <= kMany);
+        int c0, b, tile, h, np;
+        auto item = [&](int k) {
+            c0 = base + k * gridDim.x;
+            const int entry = __shfl_sync(0xffffffffu, ds.x, k);
+            h = __shfl_sync(0xffffffffu, ds.y, k);
+            np = __shfl_sync(0xffffffffu, ds.z, k);
+            b = entry / a.n_tiles;
+            tile = entry - b * a.n_tiles;
+        };
+        // piece p lies in slot 2 c0 + 1 for p = 0, 2 (c0 + p heads) after that
+        int r;
+        auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p * a.heads)) * a.R + r; };
+        float M, L, acc[NC];
+        auto top = [&] {
+            M = -INFINITY;
+            for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
 #pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-#pragma unroll
-    for (int i = 0; i < NC; ++i) acc[i] = 0.f;
-    if (in) {
-#pragma unroll 2
-        for (int p = ps; p < np; p += PS) {
-            const float2 ml = a.part_ml[slot(p)];
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            L = fmaf(w, ml.y, L);
-            const float* src = a.part_o + slot(p) * a.d;
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (lane + 32 * i < a.d) acc[i] = fmaf(w, src[lane + 32 * i], acc[i]);
-        }
-    }
-    const int64_t o = in ? paged_out_row(a, b, tile, h, r) : -1;
-    if (PS > 1) {
-        if (lane == 0) sh[warp][0] = L;
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (lane + 32 * i < a.d) so[warp][lane + 32 * i] = acc[i];
-        __syncthreads();
-        if (ps > 0) return;
-#pragma unroll
-        for (int w = 1; w < PS; ++w) {
-            L += sh[warp + w][0];
+            for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        };
+        auto store = [&] {
+            const int64_t o = paged_out_row(a, b, tile, h, r);
+            const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                if (lane + 32 * i < a.d) acc[i] += so[warp + w][lane + 32 * i];
+                if (lane + 32 * i < a.d) paged_store(a, o * a.d + lane + 32 * i, acc[i] * inv);
+            if (lane == 0) paged_store_lse(a, o, b, tile, h, r, M, L);
+        };
+        for (unsigned todo = many; todo; todo &= todo - 1) {
+            item(__ffs(todo) - 1);
+            for (r = blockIdx.y; r < paged_rows(a, tile); r += gridDim.y) {
+                top();
+                join_pieces<NC>(a, slot, warp, kJoinWarps, np, M, L, acc);
+                __syncthreads();  // the row before
+                if (lane == 0) sh[warp] = L;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) so[warp][lane + 32 * i] = acc[i];
+                __syncthreads();
+                if (warp > 0) continue;
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    L += sh[w];
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) acc[i] += so[w][lane + 32 * i];
+                }
+                store();
+            }
+        }
+        // rows of the other items: task t of all of theirs goes to warp t of the CTAs of this column
+        int t = blockIdx.y * kJoinWarps + warp;
+        for (unsigned todo = few; todo; todo &= todo - 1) {
+            item(__ffs(todo) - 1);
+            for (; t < paged_rows(a, tile); t += gridDim.y * kJoinWarps) {
+                r = t;
+                top();
+                join_pieces<NC>(a, slot, 0, 1, np, M, L, acc);
+                store();
+            }
+            t -= paged_rows(a, tile);
         }
     }
-    if (o < 0) return;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-        if (lane + 32 * i < a.d) paged_store(a, o * a.d + lane + 32 * i, acc[i] * inv);
-    if (lane == 0) paged_store_lse(a, o, b, tile, h, r, M, L);
 }
 
 constexpr int kWeightThreads = 256;
+constexpr int kWeightRows = 256;  // rows whose log-sum-exp and query are held at a time
 
 // acc_out[b][h][j] = acc[b][h][j] + the sum over the key head's queries of exp(s_j - lse), from the
-// logits that the attention kernel left: one thread per cached token, so the sum has one order.
+// logits that the attention kernel left: a thread has V neighbouring tokens and all rows in order, so the sum has
+// one order.  Reads 4 bytes a (token, row), mostly from L2.
+template <int V>
 __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttnArgs a)
 {
+    __shared__ float z[kWeightRows];
+    __shared__ RowBounds rb[kWeightRows];
+    const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int j = (blockIdx.x * kWeightThreads + tid) * V;
     pdl_launch_dependents();
     pdl_wait();
-    const int j = blockIdx.x * kWeightThreads + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
-    if (j >= a.cap) return;
     const int64_t g = (int64_t)b * a.n_kv + h, at = g * a.cap + j;
     const int rows = a.nq * a.G;
-    const float* s = a.logits + g * rows * a.cap + j;
-    const float* z = a.lse2 + g * rows;
-    float w = 0.f;
-    for (int i = 0; i < a.nq; ++i) {
-        if (!paged_visible(paged_bounds(a, b, i), j)) continue;
-        for (int r = i * a.G; r < (i + 1) * a.G; ++r) {
-            // every visible logit was written; -inf (a token without a page) weighs nothing,
-            // and with no visible row at all lse is -inf too
-            const float x = s[(int64_t)r * a.cap];
-            if (x != -INFINITY) w += exp2f(x - z[r]);
+    float w[V] = {};
+    for (int r0 = 0; r0 < rows; r0 += kWeightRows) {
+        const int n = min(kWeightRows, rows - r0);
+        __syncthreads();
+        for (int r = tid; r < n; r += kWeightThreads) {
+            z[r] = a.lse2[g * rows + r0 + r];
+            rb[r] = paged_bounds(a, b, (r0 + r) / a.G);
+        }
+        __syncthreads();
+        if (j >= a.cap) continue;
+        const float* s = a.logits + (g * rows + r0) * a.cap + j;
+#pragma unroll 4
+        for (int r = 0; r < n; ++r) {
+            float x[V];
+            if constexpr (V == 4) {
+                const float4 y = __ldcs(reinterpret_cast<const float4*>(s + (int64_t)r * a.cap));
+                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+            } else {
+                x[0] = s[(int64_t)r * a.cap];
+            }
+            // every visible logit was written; -inf (a token without a page) weighs nothing, and with no
+            // visible row at all lse is -inf too
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (paged_visible(rb[r], j + i) && x[i] != -INFINITY) w[i] += exp2f(x[i] - z[r]);
         }
     }
-    a.acc_out[at] = a.acc[at] + w;
+    if (j >= a.cap) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.acc_out[at + i] = a.acc[at + i] + w[i];
 }
 
 }  // namespace
@@ -254,8 +324,15 @@ static PagedShape paged_shape(int dtype, bool wide, bool boxes, int rows, int d)
     s.unit = kSimtUnit;
     s.min_units = kSimtWarps;
     s.item_units = 2;
-    s.grid = 2 * kNumSMs;
+    s.workers = 2 * kNumSMs;
     return s;
+}
+
+// Places of a list of the schedule, at most.
+static int64_t paged_places(const PagedShape& s, int B, int nq, int G, int n_kv, int64_t cap)
+{
+    const int64_t tiles = ((int64_t)nq * G + s.R - 1) / s.R;
+    return (std::max<int64_t>(1, (cap + s.unit - 1) / s.unit) + s.item_units) * B * tiles * (s.by_head ? 1 : n_kv);
 }
 
 // Workspace layout, from the sizes alone: room for every kernel that a call of these sizes may run on.
@@ -266,13 +343,15 @@ struct PagedPlan {
 static PagedPlan paged_plan(int B, int nq, int G, int n_kv, int d, int64_t cap, bool weights)
 {
     PagedPlan p{};
-    size_t slots = 0;  // rows of partial results
+    size_t slots = 0, workers = 0;  // rows of partial results, descriptions
     for (int dtype : {CSA_BF16, CSA_F32})
         for (int way = 0; way < 3; ++way) {
             const PagedShape s = paged_shape(dtype, way > 0, way > 1, nq * G, d);
-            slots = std::max(slots, (size_t)2 * s.grid * s.R);
+            const size_t lists = s.by_head ? n_kv : 1, runs = paged_runs(s, lists, paged_places(s, B, nq, G, n_kv, cap));
+            workers = std::max(workers, runs * lists);
+            if (runs > 1) slots = std::max(slots, 2 * runs * lists * s.R);  // a single run cuts nothing
         }
-    size_t at = 256 + align_up(sizeof(int4) * kPagedMaxCtas, 256);
+    size_t at = 256 + align_up(sizeof(int4) * workers, 256);
     p.part_ml = at;
     at += align_up(slots * sizeof(float2), 256);
     p.part_o = at;
@@ -339,9 +418,8 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     const PagedShape sp = paged_shape(dtype, wide, paged_prompt_takes(pl, n_kv, d), nq * G, d);
     a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units; a.item_units = sp.item_units;
     a.n_tiles = (nq * G + sp.R - 1) / sp.R;
-    // no more CTAs than the capacity has units
-    const int64_t units = std::max<int64_t>(1, (cap + sp.unit - 1) / sp.unit) * B * n_kv * a.n_tiles;
-    a.grid = (int)std::max<int64_t>(1, std::min<int64_t>(sp.grid, units / sp.min_units));
+    a.heads = sp.by_head ? n_kv : 1;
+    a.runs = paged_runs(sp, a.heads, paged_places(sp, B, nq, G, n_kv, cap));
     char* ws = static_cast<char*>(workspace);
     a.status = reinterpret_cast<uint32_t*>(ws);
     a.desc = reinterpret_cast<int4*>(ws + 256);
@@ -358,22 +436,28 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
         const size_t smem =
             ((size_t)a.R * d + std::max<size_t>((size_t)kSimtWarps * a.R * d, kSimtWarps * kSimtUnit * a.R)) * sizeof(float);
         if (dtype == CSA_BF16)
-            launch_pdl(paged_attn_simt<__nv_bfloat16>, dim3(a.grid), dim3(kSimtThreads), smem, s, a);
+            launch_pdl(paged_attn_simt<__nv_bfloat16>, dim3(a.runs), dim3(kSimtThreads), smem, s, a);
         else
-            launch_pdl(paged_attn_simt<float>, dim3(a.grid), dim3(kSimtThreads), smem, s, a);
+            launch_pdl(paged_attn_simt<float>, dim3(a.runs), dim3(kSimtThreads), smem, s, a);
         st = launch_status();
     } else {
         st = sp.kind == kPagedPrompt ? launch_paged_prompt(a, sp, s) : launch_paged_decode(a, sp, s);
     }
     if (st != CSA_OK) return st;
-    const int rows = std::min(a.R, nq * G);
-    if (sp.kind == kPagedPrompt)
-        launch_pdl(paged_attn_combine<1>, dim3(a.grid, (rows + 7) / 8), dim3(kJoinThreads), 0, s, a);
+    // one wave of CTAs along x; nothing is cut into a single run, but the status is written
+    const int rows = std::min(a.R, nq * G), columns = std::min(a.runs * a.heads, kNumSMs);
+    const dim3 grid(a.runs > 1 ? columns : 1, a.runs > 1 ? std::min(rows, 32) : 1);
+    if (d <= 128)
+        launch_pdl(paged_attn_combine<4>, grid, dim3(kJoinThreads), 0, s, a);
     else
-        launch_pdl(paged_attn_combine<4>, dim3(a.grid, (rows + 1) / 2), dim3(kJoinThreads), 0, s, a);
+        launch_pdl(paged_attn_combine<8>, grid, dim3(kJoinThreads), 0, s, a);
     st = launch_status();
     if (st != CSA_OK || !acc || cap == 0) return st;
-    launch_pdl(paged_weights_kernel, dim3((unsigned)((cap + kWeightThreads - 1) / kWeightThreads), n_kv, B),
-               dim3(kWeightThreads), 0, s, a);
+    const int wide_v = cap % 4 == 0 ? 4 : 1;  // rows of logits start on 16 bytes
+    const dim3 tokens((unsigned)((cap + wide_v * kWeightThreads - 1) / (wide_v * kWeightThreads)), n_kv, B);
+    if (wide_v == 4)
+        launch_pdl(paged_weights_kernel<4>, tokens, dim3(kWeightThreads), 0, s, a);
+    else
+        launch_pdl(paged_weights_kernel<1>, tokens, dim3(kWeightThreads), 0, s, a);
     return launch_status();
 }

@@ -1,14 +1,14 @@
 // paged_attn for few query rows: the decode kernels, bound by the bytes of the cache.
 //
-// A CTA has kWarps warps in token groups.  A group owns every kWarps / WR-th unit (a few cached
-// tokens) of the CTA's run and a ring of stages that its lanes fill with 16-byte cp.async, two
-// units ahead of the one being used; a token that no row sees, or without a page, is zero-filled and
-// not read.  Each group keeps its own running maximum, sum and output, so groups never wait for
-// one another inside a run; they are joined once at its end.
+// A CTA has 8 warps (4 for wide heads), each a worker of its own with a run of units (a few cached tokens) of one
+// key head and a ring of stages that its lanes fill with 16-byte cp.async, two units ahead of the one being used; a
+// token that no row sees, or without a page, is zero-filled and not read.  The warps of a CTA have the same run of
+// neighbouring heads, whose rows lie together in a [row][head] page.  No warp waits for another: a run's
+// output, or its partial result, goes from the warp's registers to memory.
 //   bf16: the rows are the 16-row operand of mma.sync (m16n8k16), K is its B operand as stored,
 //         V through transposing ldmatrix.  The weights go to the second product as two bf16
 //         parts (hi + lo), which keeps 16 bits of them at the price of tensor work that is idle anyway.
-//         WR > 1: WR warps of a group have 16 rows each and share the group's ring.
+//         WR > 1: WR warps have 16 rows each and share a ring; they are one worker.
 //   fp32: plain FMAs, a token spread over LT lanes, RT rows in registers.
 #include "cluster.cuh"
 #include "paged.cuh"
@@ -16,8 +16,6 @@
 
 namespace csa {
 namespace {
-
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 
 CSA_DEV void cp16(uint32_t dst, const void* src, bool take)
 {
@@ -109,67 +107,66 @@ struct Ring {
 
 template <int DP, int WR>
 struct MmaShape {
-    static constexpr int kWT = kWarps / WR;                        // token groups
+    static constexpr int kWarps = DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
+    static constexpr int kGroups = kWarps / WR;                    // workers of a CTA
     static constexpr int kU = DP == 64 || (WR > 1 && DP == 128) ? 32 : 16;
     static constexpr int kStages = WR == 4 ? 6 : 3;
     static constexpr int kRows = 16 * WR;
-    static constexpr int kRing = kWT * kStages * 2 * kU * DP * 2;  // bytes
-    static constexpr int kQ = DP == 256 ? kRows * DP * 2 : 0;      // wide heads: q in shared memory
-    static constexpr int kJoin = kWT * kRows * (DP + 8) * 4;       // over the ring at a segment's end
-    static constexpr int kSmem = kQ + (kRing > kJoin ? kRing : kJoin);
-    static constexpr int kCtas = kSmem <= 112 * 1024 ? 2 : 1;      // on an SM
+    static constexpr int kRing = kGroups * kStages * 2 * kU * DP * 2;    // bytes
+    static constexpr int kQ = DP == 256 ? kGroups * kRows * DP * 2 : 0;  // wide heads: q in shared memory
+    static constexpr int kSmem = kQ + kRing;
 };
 
 template <int DP, int WR>
-__global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_mma(PagedAttnArgs a)
+__global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, 1) paged_attn_mma(PagedAttnArgs a)
 {
     using S = MmaShape<DP, WR>;
-    constexpr int U = S::kU, R = S::kRows, WT = S::kWT, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
+    constexpr int U = S::kU, R = S::kRows, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ PagedScratch<kThreads, 1> sh;
-    __shared__ float sm_m[WT * R], sm_l[WT * R];
-    __shared__ uint32_t masks[WT * NS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-    const int group = warp / WR, wr = warp % WR;
+    __shared__ PagedScratch<S::kThreads, 1> sh;
+    __shared__ uint32_t masks[S::kGroups * NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = warp / WR, wr = warp % WR, worker = blockIdx.x * S::kGroups + group;
+    const int run = worker / a.heads;
     uint8_t* sring = smem + S::kQ;
-    float* so = reinterpret_cast<float*>(sring);
     pdl_launch_dependents();
     pdl_wait();
-    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
+    if (run < a.runs && wr == 0 && lane == 0) a.desc[worker] = make_int4(-1, 0, 0, 0);
     PagedCursor c;
-    if (!paged_schedule<kThreads, 1>(a, cta, sh, c)) return;
+    if (!paged_schedule<S::kThreads, 1, true>(a, run, sh, c)) return;
+    c.h = worker - run * a.heads;
     Ring<ROWB, U, WR> ring;
     ring.base = tc::smem_u32(sring) + group * (NS * ring.kStage);
     ring.masks = masks + group * NS;
     ring.row_bytes = a.d * 2;
     ring.lane = wr * 32 + lane;
+    ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
+    ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    const uint32_t sq = tc::smem_u32(smem) + wr * 16 * ROWB;
+    uint8_t* my_q = smem + (group * R + wr * 16) * ROWB;  // this warp's rows (wide heads)
+    const uint32_t sq = tc::smem_u32(my_q);
     const int r0 = wr * 16 + (lane >> 2);  // this lane's rows: r0 and r0 + 8
     while (true) {
-        const PagedSegment sg = paged_segment(a, c, cta);
+        const PagedSegment sg = paged_segment(a, c, worker);
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
-        if (tid == 0) paged_describe(a, c, sg, cta);
+        if (wr == 0 && lane == 0) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
-        ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
-        ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
-        const int first = sg.u0 + group, n_u = first < sg.u1 ? (sg.u1 - first + WT - 1) / WT : 0;
+        const int n_u = sg.u1 - sg.u0;
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) {
-            if (s < n_u) ring.load(a, en, first + s * WT, s, 2);
+            if (s < n_u) ring.load(a, en, sg.u0 + s, s, 2);
             cp_commit();
         }
         uint32_t qf[DP == 256 ? 1 : KS][4];
         if constexpr (DP == 256) {
-            for (int x = tid; x < R * (DP / 8); x += kThreads) {
+            for (int x = lane; x < 16 * (DP / 8); x += 32) {
                 const int r = x / (DP / 8), ch = x % (DP / 8);
-                const int64_t o = paged_out_row(a, en.b, en.tile, c.h, r);
+                const int64_t o = paged_out_row(a, en.b, en.tile, c.h, wr * 16 + r);
                 const bool in = o >= 0 && ch * 8 < a.d;
                 const uint4 v = in ? *reinterpret_cast<const uint4*>(q + o * a.d + ch * 8) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(smem + at16<ROWB>(r, ch)) = v;
+                *reinterpret_cast<uint4*>(my_q + at16<ROWB>(r, ch)) = v;
             }
-            __syncthreads();
+            __syncwarp();
         } else {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -206,10 +203,10 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
         for (int i = 0; i < n_u; ++i) {
             cp_wait<NS - 2>();
             group_sync<WR>(group);
-            const int u = first + i * WT;
+            const int u = sg.u0 + i;
             {
                 const int nx = st == 0 ? NS - 1 : st - 1;
-                if (i + NS - 1 < n_u) ring.load(a, en, u + (NS - 1) * WT, nx, 2);
+                if (i + NS - 1 < n_u) ring.load(a, en, u + NS - 1, nx, 2);
                 cp_commit();
             }
             const uint32_t sk = ring.base + st * ring.kStage, sv = sk + U * ROWB;
@@ -303,26 +300,40 @@ __global__ void __launch_bounds__(kThreads, MmaShape<DP, WR>::kCtas) paged_attn_
             }
         }
         cp_wait<0>();
-        __syncthreads();  // every group is done with its ring: so lies over it
+        group_sync<WR>(group);  // the ring is filled anew
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+            const int r = r0 + 8 * half;
             l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
             l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-            if ((lane & 3) == 0) {
-                sm_m[group * R + r0 + 8 * half] = m[half];
-                sm_l[group * R + r0 + 8 * half] = l[half];
-            }
-            if (row_in[half]) {
+            if (!row_in[half]) continue;
+            if (sg.whole) {
+                const int64_t at = paged_out_row(a, en.b, en.tile, c.h, r);
+                const float inv = l[half] > 0.f ? 1.f / l[half] : 0.f;
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n)
-                    *reinterpret_cast<float2*>(so + (group * R + r0 + 8 * half) * (DP + 8) + n * 8 + 2 * (lane & 3)) =
-                        make_float2(o[n][2 * half], o[n][2 * half + 1]);
+                for (int n = 0; n < DP / 8; ++n) {
+                    const int col = n * 8 + 2 * (lane & 3);
+                    const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
+                    if (col >= a.d) continue;
+                    if (a.out_bf16)
+                        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at * a.d + col) = pack2(x, y);
+                    else
+                        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at * a.d + col) = make_float2(x, y);
+                }
+                if ((lane & 3) == 0) paged_store_lse(a, at, en.b, en.tile, c.h, r, m[half], l[half]);
+            } else {
+                const int64_t at = (int64_t)sg.slot * R + r;
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n) {
+                    const int col = n * 8 + 2 * (lane & 3);
+                    if (col < a.d)
+                        *reinterpret_cast<float2*>(a.part_o + at * a.d + col) =
+                            make_float2(o[n][2 * half], o[n][2 * half + 1]);
+                }
+                if ((lane & 3) == 0) a.part_ml[at] = make_float2(m[half], l[half]);
             }
         }
-        __syncthreads();
-        paged_finish_segment<kThreads, WT, R>(a, c, sg, so, DP + 8, sm_m, sm_l);
-        __syncthreads();
-        if (!paged_next<1>(a, c, sg)) break;
+        if (!paged_next<1, true>(a, c, sg)) break;
     }
 }
 
@@ -333,47 +344,45 @@ struct F32Shape {
     static constexpr int kNG = 32 / kLT;     // tokens at a time
     static constexpr int kU = 1024 / DP;     // tokens of a unit: 8 KB of K and V
     static constexpr int kStages = 3;
-    static constexpr int kRing = kWarps * kStages * 2 * kU * DP * 4;
-    static constexpr int kJoin = kWarps * RT * (DP + 4) * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kWarps = 8, kThreads = 32 * kWarps;
+    static constexpr int kSmem = kWarps * kStages * 2 * kU * DP * 4;
 };
 
 template <int DP, int RT>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
+__global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(PagedAttnArgs a)
 {
     using S = F32Shape<DP, RT>;
     constexpr int U = S::kU, NS = S::kStages, EL = S::kEL, LT = S::kLT, NG = S::kNG, TG = U / NG, ROWB = DP * 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ PagedScratch<kThreads, 1> sh;
-    __shared__ float sm_m[kWarps * RT], sm_l[kWarps * RT];
-    __shared__ uint32_t masks[kWarps * NS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    __shared__ PagedScratch<S::kThreads, 1> sh;
+    __shared__ uint32_t masks[S::kWarps * NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, worker = blockIdx.x * S::kWarps + warp;
+    const int run = worker / a.heads;
     const int g = lane / LT, e = lane % LT;
-    float* so = reinterpret_cast<float*>(smem);
     pdl_launch_dependents();
     pdl_wait();
-    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
+    if (run < a.runs && lane == 0) a.desc[worker] = make_int4(-1, 0, 0, 0);
     PagedCursor c;
-    if (!paged_schedule<kThreads, 1>(a, cta, sh, c)) return;
+    if (!paged_schedule<S::kThreads, 1, true>(a, run, sh, c)) return;
+    c.h = worker - run * a.heads;
     Ring<ROWB, U, 1> ring;
     ring.base = tc::smem_u32(smem) + warp * (NS * ring.kStage);
     ring.masks = masks + warp * NS;
     ring.row_bytes = a.d * 4;
     ring.lane = lane;
+    ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 4;
+    ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 4;
     const uint8_t* my = smem + warp * (NS * ring.kStage);
     const float* q = static_cast<const float*>(a.q);
     while (true) {
-        const PagedSegment sg = paged_segment(a, c, cta);
+        const PagedSegment sg = paged_segment(a, c, worker);
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
-        if (tid == 0) paged_describe(a, c, sg, cta);
+        if (lane == 0) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
-        ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 4;
-        ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 4;
-        const int first = sg.u0 + warp, n_u = first < sg.u1 ? (sg.u1 - first + kWarps - 1) / kWarps : 0;
+        const int n_u = sg.u1 - sg.u0;
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) {
-            if (s < n_u) ring.load(a, en, first + s * kWarps, s, 4);
+            if (s < n_u) ring.load(a, en, sg.u0 + s, s, 4);
             cp_commit();
         }
         float2 qr[RT][EL / 2], o[RT][EL / 2];
@@ -397,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
         for (int i = 0; i < n_u; ++i) {
             cp_wait<NS - 2>();
             __syncwarp();
-            const int u = first + i * kWarps;
+            const int u = sg.u0 + i;
             {
                 const int nx = st == 0 ? NS - 1 : st - 1;
-                if (i + NS - 1 < n_u) ring.load(a, en, u + (NS - 1) * kWarps, nx, 4);
+                if (i + NS - 1 < n_u) ring.load(a, en, u + NS - 1, nx, 4);
                 cp_commit();
             }
             const uint8_t *sk = my + st * ring.kStage, *sv = sk + U * ROWB;
@@ -485,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
             }
         }
         cp_wait<0>();
-        __syncthreads();
-        // join the NG token groups of the warp, then the warps through shared memory
+        __syncwarp();  // the ring is filled anew
+        // join the NG token groups of the warp
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             float M = m[r];
@@ -505,43 +514,54 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_f32(PagedAttnArgs a)
                     o[r][x].x += __shfl_xor_sync(0xffffffffu, o[r][x].x, y);
                     o[r][x].y += __shfl_xor_sync(0xffffffffu, o[r][x].y, y);
                 }
-                if (g == 0)
-                    *reinterpret_cast<float2*>(so + (warp * RT + r) * (DP + 4) + (e + LT * (x / 2)) * 4 + 2 * (x & 1)) =
-                        o[r][x];
             }
-            if (lane == 0) {
-                sm_m[warp * RT + r] = M;
-                sm_l[warp * RT + r] = l[r];
+            if (g == 0 && r < paged_rows(a, en.tile)) {
+                const int64_t at = sg.whole ? paged_out_row(a, en.b, en.tile, c.h, r) : (int64_t)sg.slot * RT + r;
+                float* to = (sg.whole ? static_cast<float*>(a.out) : a.part_o) + at * a.d;
+                const float inv = sg.whole ? (l[r] > 0.f ? 1.f / l[r] : 0.f) : 1.f;
+#pragma unroll
+                for (int x = 0; x < EL / 4; ++x) {
+                    const int col = (e + LT * x) * 4;
+                    if (col < a.d)
+                        *reinterpret_cast<float4*>(to + col) = make_float4(o[r][2 * x].x * inv, o[r][2 * x].y * inv,
+                                                                           o[r][2 * x + 1].x * inv, o[r][2 * x + 1].y * inv);
+                }
+                if (e == 0) {
+                    if (sg.whole)
+                        paged_store_lse(a, at, en.b, en.tile, c.h, r, M, l[r]);
+                    else
+                        a.part_ml[at] = make_float2(M, l[r]);
+                }
             }
+            __syncwarp();
         }
-        __syncthreads();
-        paged_finish_segment<kThreads, kWarps, RT>(a, c, sg, so, DP + 4, sm_m, sm_l);
-        __syncthreads();
-        if (!paged_next<1>(a, c, sg)) break;
+        if (!paged_next<1, true>(a, c, sg)) break;
     }
 }
 
 template <typename F>
-int launch(F* kern, int smem, const PagedAttnArgs& a, cudaStream_t stream)
+int launch(F* kern, int threads, int workers, int smem, const PagedAttnArgs& a, cudaStream_t stream)
 {
     // per device and idempotent; no state is kept between calls
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return CSA_ERR_CUDA;
     }
-    launch_pdl(kern, dim3(a.grid), dim3(kThreads), smem, stream, a);
+    launch_pdl(kern, dim3((a.runs * a.heads + workers - 1) / workers), dim3(threads), smem, stream, a);
     return launch_status();
 }
 
 template <int DP, int WR>
 int launch_mma(const PagedAttnArgs& a, cudaStream_t stream)
 {
-    return launch(paged_attn_mma<DP, WR>, MmaShape<DP, WR>::kSmem, a, stream);
+    using S = MmaShape<DP, WR>;
+    return launch(paged_attn_mma<DP, WR>, S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
 template <int DP, int RT>
 int launch_f32(const PagedAttnArgs& a, cudaStream_t stream)
 {
-    return launch(paged_attn_f32<DP, RT>, F32Shape<DP, RT>::kSmem, a, stream);
+    using S = F32Shape<DP, RT>;
+    return launch(paged_attn_f32<DP, RT>, S::kThreads, S::kWarps, S::kSmem, a, stream);
 }
 
 }  // namespace
@@ -551,21 +571,22 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
 {
     PagedShape s{};
     s.DP = d <= 64 ? 64 : d <= 128 ? 128 : 256;
+    s.by_head = true;
     if (dtype == CSA_BF16) {
         s.kind = kPagedMma;
         s.WR = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         s.R = 16 * s.WR;
         s.unit = s.DP == 64 || (s.WR > 1 && s.DP == 128) ? 32 : 16;
-        s.min_units = 2 * (kWarps / s.WR);
-        s.item_units = s.WR == 1 ? 8 : 4;
-        s.grid = (s.DP == 256 && s.WR == 1 ? 1 : 2) * kNumSMs;
+        s.min_units = 6;
+        s.item_units = 4;
+        s.workers = (s.DP == 256 ? 4 : 8) / s.WR * kNumSMs;
     } else {
         s.kind = kPagedF32;
         s.WR = s.R = rows <= 4 ? 4 : 8;
         s.unit = 1024 / s.DP;
-        s.min_units = 2 * kWarps;
-        s.item_units = 8;
-        s.grid = 2 * kNumSMs;
+        s.min_units = 6;
+        s.item_units = 4;
+        s.workers = 8 * kNumSMs;
     }
     return s;
 }

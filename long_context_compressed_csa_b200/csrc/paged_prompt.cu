@@ -161,7 +161,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     pdl_wait();
     if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     PagedCursor c;
-    const bool some = paged_schedule<kThreads, 8>(a, cta, sh, c);
+    const bool some = paged_schedule<kThreads, 8, false>(a, cta, sh, c);
     // false after a timeout; the caller leaves its loops
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         // no sleep between the polls: a wake-up costs more than the waits of this kernel last
@@ -501,7 +501,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     }
                     if (!ok) break;
                 }
-                if (!ok || !paged_next<32>(a, c, sg)) break;
+                if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
             // no copy is in flight when the CTA ends: on the normal path the products have waited for them
             if (!ok)
@@ -588,7 +588,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         __syncwarp();
                     }
                 }
-                if (!ok || !paged_next<32>(a, c, sg)) break;
+                if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
         }
     }
@@ -609,7 +609,7 @@ int launch(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, i
         cudaGetLastError();
         return CSA_ERR_CUDA;
     }
-    launch_pdl(paged_attn_prompt<DP>, dim3(a.grid), dim3(kThreads), smem, stream, k, v, a, box_rows);
+    launch_pdl(paged_attn_prompt<DP>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
     return launch_status();
 }
 
@@ -633,7 +633,7 @@ PagedShape paged_prompt_shape(int d)
     s.unit = kT;
     s.min_units = 2;
     s.item_units = 2;
-    s.grid = kNumSMs;
+    s.workers = kNumSMs;
     return s;
 }
 
