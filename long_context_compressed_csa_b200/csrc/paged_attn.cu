@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "paged.cuh"
+#include "tc_utils.cuh"
 
 namespace csa {
 
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 }
 
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinColumns = 37;  // 32 x 37: every worker of a full GPU in one look
 
 // Pieces p0, p0 + step, ... of a row: their weighted sum, four under way at once.  slot(p): where piece p lies.
 template <int NC, typename F>
@@ -260,47 +262,56 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
 }
 
 constexpr int kWeightThreads = 256;
-constexpr int kWeightRows = 256;  // rows whose log-sum-exp and query are held at a time
+constexpr int kWeightRows = 1024;  // rows whose log-sum-exp is held at a time
 
 // acc_out[b][h][j] = acc[b][h][j] + the sum over the key head's queries of exp(s_j - lse), from the
 // logits that the attention kernel left: a thread has V neighbouring tokens and all rows in order, so the sum has
-// one order.  Reads 4 bytes a (token, row), mostly from L2.
+// one order.  Reads 4 bytes a (token, row), mostly from L2; bound by the launch and those reads.
 template <int V>
 __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttnArgs a)
 {
     __shared__ float z[kWeightRows];
-    __shared__ RowBounds rb[kWeightRows];
     const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int j = (blockIdx.x * kWeightThreads + tid) * V;
     pdl_launch_dependents();
     pdl_wait();
     const int64_t g = (int64_t)b * a.n_kv + h, at = g * a.cap + j;
-    const int rows = a.nq * a.G;
+    const int rows = a.nq * a.G, step = max(1, kWeightRows / a.G);  // queries at a time
     float w[V] = {};
-    for (int r0 = 0; r0 < rows; r0 += kWeightRows) {
-        const int n = min(kWeightRows, rows - r0);
-        __syncthreads();
-        for (int r = tid; r < n; r += kWeightThreads) {
-            z[r] = a.lse2[g * rows + r0 + r];
-            rb[r] = paged_bounds(a, b, (r0 + r) / a.G);
-        }
-        __syncthreads();
-        if (j >= a.cap) continue;
-        const float* s = a.logits + (g * rows + r0) * a.cap + j;
-#pragma unroll 4
-        for (int r = 0; r < n; ++r) {
-            float x[V];
-            if constexpr (V == 4) {
-                const float4 y = __ldcs(reinterpret_cast<const float4*>(s + (int64_t)r * a.cap));
-                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-            } else {
-                x[0] = s[(int64_t)r * a.cap];
+    for (int i0 = 0; i0 < a.nq; i0 += step) {
+        const int i1 = min(a.nq, i0 + step);
+        // held in parts where one query has more rows than that
+        for (int g0 = 0; g0 < a.G; g0 += kWeightRows) {
+            const int gn = min(kWeightRows, a.G - g0), r0 = i0 * a.G + g0, n = step > 1 ? (i1 - i0) * a.G : gn;
+            __syncthreads();
+            for (int r = tid; r < n; r += kWeightThreads) {
+                // a row that sees nothing has lse = -inf: its logits, all -inf, weigh nothing
+                const float x = a.lse2[g * rows + r0 + r];
+                z[r] = x == -INFINITY ? INFINITY : x;
             }
-            // every visible logit was written; -inf (a token without a page) weighs nothing, and with no
-            // visible row at all lse is -inf too
+            __syncthreads();
+            if (j >= a.cap) continue;
+            for (int i = i0; i < i1; ++i) {
+                const RowBounds rb = paged_bounds(a, b, i);
+                bool see[V], any = false;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (paged_visible(rb[r], j + i) && x[i] != -INFINITY) w[i] += exp2f(x[i] - z[r]);
+                for (int x = 0; x < V; ++x) any |= see[x] = paged_visible(rb, j + x);
+                if (!any) continue;  // logits that were never written
+                const float* s = a.logits + (g * rows + i * a.G + g0) * a.cap + j;
+#pragma unroll 8
+                for (int r = 0; r < gn; ++r) {
+                    float x[V];
+                    if constexpr (V == 4) {
+                        const float4 y = __ldcs(reinterpret_cast<const float4*>(s + (int64_t)r * a.cap));
+                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+                    } else {
+                        x[0] = s[(int64_t)r * a.cap];
+                    }
+                    const float zr = z[(i - i0) * a.G + r];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) w[k] += see[k] ? tc::ex2_approx(x[k] - zr) : 0.f;
+                }
+            }
         }
     }
     if (j >= a.cap) return;
@@ -444,9 +455,13 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
         st = sp.kind == kPagedPrompt ? launch_paged_prompt(a, sp, s) : launch_paged_decode(a, sp, s);
     }
     if (st != CSA_OK) return st;
-    // one wave of CTAs along x; nothing is cut into a single run, but the status is written
-    const int rows = std::min(a.R, nq * G), columns = std::min(a.runs * a.heads, kNumSMs);
-    const dim3 grid(a.runs > 1 ? columns : 1, a.runs > 1 ? std::min(rows, 32) : 1);
+    // A decode call's rows are few and its items may have many pieces: a CTA for each row, an SM for each column (64
+    // windows of 1024 tokens: 64 us, 68 with the other grid).  A prompt's rows are many: one wave of three CTAs an SM (64
+    // rows of 16 sequences: 50 us, 57).  Nothing is cut into a single run, but the status is written.
+    const int rows = std::min(a.R, nq * G), workers = a.runs * a.heads;
+    const dim3 grid = a.runs == 1 ? dim3(1)
+                      : rows <= 16 ? dim3(std::min(workers, kNumSMs), rows)
+                                   : dim3(std::min(workers, kJoinColumns), 3 * kNumSMs / kJoinColumns);
     if (d <= 128)
         launch_pdl(paged_attn_combine<4>, grid, dim3(kJoinThreads), 0, s, a);
     else
