@@ -383,6 +383,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _i32(*xs):
+    """Counts as C ints: what does not fit is refused, not cut to 32 bits."""
+    out = tuple(map(int, xs))
+    for x in out:
+        if not -2**31 <= x < 2**31:
+            raise ValueError("%d does not fit in 32 bits" % x)
+    return out
+
+
 def _pool(K, V, table, B):
     """Strides and sizes of the pools K, V [n_pages, page, n_kv, d] (any page, row and head
     strides, so a permuted [n_pages, n_kv, page, d] pool too) and of the page table [B, max_pages]."""
@@ -415,7 +424,7 @@ def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
 
 def paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, weights=False) -> int:
     """Bytes of workspace of paged_attn; cap = max_pages * page, weights: with acc."""
-    return int(library().paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, 1 if weights else 0))
+    return int(library().paged_attn_workspace_size(*_i32(B, nq, n_h, n_kv, d), int(cap), 1 if weights else 0))
 
 
 def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.0, n_win=0, n_sink=0, acc=None,
@@ -441,8 +450,8 @@ def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.
             assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, cap)
     assert workspace.is_contiguous()
     _check("paged_attn", library().paged_attn(
-        q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), *pool, t.data_ptr(), B, nq, n_h, n_kv, d, n_win, n_sink,
-        scale, out.data_ptr(), _at(lse), _at(acc), _at(acc_out), workspace.data_ptr(), workspace.nbytes, _dtype(q),
+        q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), *pool, t.data_ptr(), B, nq, n_h, n_kv, d,
+        *_i32(n_win, n_sink), float(scale), out.data_ptr(), _at(lse), _at(acc), _at(acc_out), workspace.data_ptr(), workspace.nbytes, _dtype(q),
         1 if _dtype(out) == CSA_BF16 else 0, raw))
 
 
@@ -464,6 +473,6 @@ def paged_evict(K_pages, V_pages, table, lens, acc, keep, new_table, new_lens, n
         assert x.dtype == torch.float32 and x.is_contiguous() and x.shape == (B, n_kv, size)
     assert idx_out.dtype == torch.int32 and idx_out.shape == (B, n_kv, keep) and idx_out.is_contiguous()
     _check("paged_evict", library().paged_evict(
-        K_pages.data_ptr(), V_pages.data_ptr(), *pool, lens.data_ptr(), acc.data_ptr(), B, n_kv, d, keep, n_sink,
-        n_recent, new_table.data_ptr(), new_pages, new_lens.data_ptr(), new_acc.data_ptr(), idx_out.data_ptr(),
+        K_pages.data_ptr(), V_pages.data_ptr(), *pool, lens.data_ptr(), acc.data_ptr(), B, n_kv, d,
+        *_i32(keep, n_sink, n_recent), new_table.data_ptr(), new_pages, new_lens.data_ptr(), new_acc.data_ptr(), idx_out.data_ptr(),
         _dtype(K_pages), raw))

@@ -298,7 +298,7 @@ CSA_DEV void paged_store(const PagedAttnArgs& a, int64_t at, float v)
 }
 CSA_DEV void paged_store_lse(const PagedAttnArgs& a, int64_t o, int b, int tile, int h, int r, float m, float l)
 {
-    const float z = l > 0.f ? m + log2f(l) : -INFINITY;
+    const float z = l == 0.f ? -INFINITY : m + log2f(l);  // a NaN stays one
     if (a.lse) a.lse[o] = z * 0.6931471805599453f;
     if (a.lse2) a.lse2[((int64_t)b * a.n_kv + h) * (a.nq * a.G) + tile * a.R + r] = z;
 }
@@ -329,7 +329,7 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
         }
         if (sg.whole) {
             const int64_t o = paged_out_row(a, c.en.b, c.en.tile, c.h, r);
-            paged_store(a, o * a.d + col, L > 0.f ? v / L : 0.f);
+            paged_store(a, o * a.d + col, L == 0.f ? 0.f : v / L);
             if (col == 0) paged_store_lse(a, o, c.en.b, c.en.tile, c.h, r, M, L);
         } else {
             const int64_t at = (int64_t)sg.slot * R + r;

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
         };
         auto store = [&] {
             const int64_t o = paged_out_row(a, b, tile, h, r);
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
             for (int i = 0; i < NC; ++i)
                 if (lane + 32 * i < a.d) paged_store(a, o * a.d + lane + 32 * i, acc[i] * inv);
@@ -423,9 +423,9 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     a.n_win = n_win; a.n_sink = n_win > 0 ? n_sink : 0; a.cap = (int)cap;
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * kLog2e;
     a.out = out; a.out_bf16 = out_bf16; a.lse = lse;
-    // 16-byte loads: every row starts on a 16-byte boundary and is whole 16-byte words
+    // 16-byte loads and stores: every row starts on a 16-byte boundary and is whole 16-byte words
     const int64_t lds = pool_ld_page | pool_ld_row | (n_kv > 1 ? pool_ld_head : 0) | d;
-    const bool wide = aligned16(q) && aligned16(K) && aligned16(V) && lds * elem_bytes(dtype) % 16 == 0;
+    const bool wide = aligned16(q) && aligned16(K) && aligned16(V) && aligned16(out) && lds * elem_bytes(dtype) % 16 == 0;
     const PagedShape sp = paged_shape(dtype, wide, paged_prompt_takes(pl, n_kv, d), nq * G, d);
     a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units; a.item_units = sp.item_units;
     a.n_tiles = (nq * G + sp.R - 1) / sp.R;

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, 1) paged_attn_mma(
             if (!row_in[half]) continue;
             if (sg.whole) {
                 const int64_t at = paged_out_row(a, en.b, en.tile, c.h, r);
-                const float inv = l[half] > 0.f ? 1.f / l[half] : 0.f;
+                const float inv = l[half] == 0.f ? 0.f : 1.f / l[half];
 #pragma unroll
                 for (int n = 0; n < DP / 8; ++n) {
                     const int col = n * 8 + 2 * (lane & 3);
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
             if (g == 0 && r < paged_rows(a, en.tile)) {
                 const int64_t at = sg.whole ? paged_out_row(a, en.b, en.tile, c.h, r) : (int64_t)sg.slot * RT + r;
                 float* to = (sg.whole ? static_cast<float*>(a.out) : a.part_o) + at * a.d;
-                const float inv = sg.whole ? (l[r] > 0.f ? 1.f / l[r] : 0.f) : 1.f;
+                const float inv = sg.whole ? (l[r] == 0.f ? 0.f : 1.f / l[r]) : 1.f;
 #pragma unroll
                 for (int x = 0; x < EL / 4; ++x) {
                     const int col = (e + LT * x) * 4;

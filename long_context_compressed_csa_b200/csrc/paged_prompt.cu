@@ -118,7 +118,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
     uint8_t* sO = sV + NS * S::kTile;      // [8 warps][32 rows][128 bytes]
-    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS];
+    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS], drained;
     // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S; by the time
     // of unit n the V stage of n - NS - 1 has been free, so n - 2 NS is long past.
     __shared__ uint32_t have[2 * NS];
@@ -128,7 +128,6 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     __shared__ PagedCursor cursors[8];     // of the softmax warps, whose registers hold S
     __shared__ volatile int failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-    pdl_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&Qfull[i], kM / 32);
@@ -142,6 +141,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             tc::mbar_init(&Vfull[i], 1);
             tc::mbar_init(&Vempty[i], 1);
         }
+        tc::mbar_init(&drained, 1);
         failed = 0;
         tc::tma_prefetch_desc(&map_k);
         tc::tma_prefetch_desc(&map_v);
@@ -155,6 +155,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
+    pdl_launch_dependents();  // with the TMEM in hand: no later kernel of the stream can wait for it and hold it up
     // S of tile w at column w kT, O at 2 kT + w DP
     auto tS = [&](int w) { return tmem + w * kT; };
     auto tO = [&](int w) { return tmem + 2 * kT + w * DP; };
@@ -398,7 +399,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (out.tile) {
                 tc::fence_after_sync();
                 const int64_t slot = (int64_t)done.slot * a.R + w * kM + r;
-                const float inv = done.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                const float inv = done.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 // through shared memory, so that a warp writes whole lines: 128 bytes of each of its rows at a time,
                 // 16-byte chunks swizzled by the row
                 uint8_t* so = sO + warp * (32 * 128);
@@ -505,7 +506,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
             // no copy is in flight when the CTA ends: on the normal path the products have waited for them
             if (!ok)
-                for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k) {
+                for (uint32_t k = n >= NS ? n - NS + 1 : 0; k <= n; ++k) {
                     wait(&Kfull[k % NS], k / NS);
                     wait(&Vfull[k % NS], k / NS);
                 }
@@ -590,8 +591,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 }
                 if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
+            if (!ok) {  // nor a product: they read shared memory and write TMEM
+                if (elect()) tc::mma_commit(&drained);
+                __syncwarp();
+                wait(&drained, 0);
+            }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     if (tid == 0 && failed) a.desc[cta].w = 1;

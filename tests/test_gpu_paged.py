@@ -543,3 +543,168 @@ def test_a_serving_run():
     for i in range(3):
         lens = [n + 1 for n in lens]
         step(1, lens, new_table, new_acc if i else None, n_win=0 if i else 16, n_sink=2)
+
+
+# ==================================================================================
+# the borders of the kernels: row tiles, boxes of pages, halves, runs and clusters
+# ==================================================================================
+@pytest.mark.parametrize("nq,G", [(16, 1), (17, 1), (4, 4), (6, 3), (127, 1), (32, 4), (43, 3), (64, 4), (257, 1), (86, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_row_tiles(nq, G, d):
+    case([nq, nq + 70], nq=nq, n_h=G, n_kv=1, d=d, seed=nq)
+
+
+@pytest.mark.parametrize("page", [4, 7, 8, 24, 40, 56, 80, 96, 100, 192])
+def test_attn_prompt_page_boxes(page):
+    case([60, 300], nq=60, n_h=6, n_kv=2, d=128, page=page, seed=page)
+    case([60, 300], nq=60, n_h=6, n_kv=2, d=128, page=page, n_win=70, n_sink=9, seed=page)
+
+
+@pytest.mark.parametrize("d", [8, 24, 40, 72, 96, 104, 120, 192])
+def test_attn_prompt_head_widths(d):
+    case([50, 190], nq=50, n_h=4, n_kv=2, d=d, seed=d)
+
+
+@pytest.mark.parametrize("n_win", [1, 2, 63, 64, 65, 127, 128, 129, 200])
+@pytest.mark.parametrize("n_sink", [0, 1, 64, 130])
+def test_attn_prompt_window_borders(n_win, n_sink):
+    case([130, 460], nq=130, n_h=2, n_kv=1, d=64, n_win=n_win, n_sink=n_sink, seed=n_win)
+
+
+def test_attn_prompts_ragged():
+    case([(53 * i) % 200 + 1 for i in range(40)], nq=30, n_h=4, n_kv=2, d=64, page=8)
+    case([900, 1, 40, 333], nq=200, n_h=8, n_kv=2, d=128, page=32)
+    case([2500], nq=70, n_h=2, n_kv=2, d=128, page=16)
+
+
+def test_attn_more_key_heads_than_workers():
+    case([20, 3], n_h=1300, n_kv=1300, d=8)
+    case([20, 3], n_h=1300, n_kv=1300, d=8, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attn_outputs_that_do_not_start_on_16_bytes(nq, dtype):
+    K, V = pools(9, 16, 2, 64, dtype, 5)
+    table = tables(2, 4, 9, 1).to(DEV)
+    t = positions([60, 45], nq).to(DEV)
+    q = randn((2, nq, 8, 64), 9, dtype).to(DEV)
+    ws = torch.empty(lib.paged_attn_workspace_size(2, nq, 8, 2, 64, 64), dtype=torch.uint8, device=DEV)
+    for odd_q in (False, True):
+        flat = torch.zeros(q.numel() + 1, dtype=dtype, device=DEV)
+        out = flat[1:].view(q.shape) if not odd_q else torch.empty_like(q)
+        flat_q = torch.zeros(q.numel() + 1, dtype=dtype, device=DEV)
+        flat_q[1:] = q.flatten()
+        lse = torch.empty(2, nq, 8, device=DEV)
+        lib.paged_attn(flat_q[1:].view(q.shape) if odd_q else q, K, V, table, t, out, ws, lse=lse)
+        check_attn(q, K, V, table, t, out, lse, 2.0 ** -16)
+        assert flat[0] == 0
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attn_nan_that_is_seen_is_told(nq, dtype):
+    K, V = pools(9, 16, 2, 64, dtype, 5)
+    table = tables(2, 4, 9, 1).to(DEV)
+    t = positions([60, 60], nq).to(DEV)
+    q = randn((2, nq, 8, 64), 9, dtype).to(DEV)
+    K[table[0, 0].long(), 3, 1, 5] = float("nan")  # token 3 of sequence 0, key head 1
+    out, lse, _ = run_attn(q, K, V, table, t)
+    bad = torch.zeros(2, 8, dtype=torch.bool, device=DEV)
+    bad[0, 4:] = True
+    assert torch.equal(lse.isnan(), bad[:, None].expand(2, nq, 8))
+    assert torch.equal(out.isnan().all(-1), out.isnan().any(-1)) and torch.equal(out.isnan().all(-1), lse.isnan())
+
+
+def test_attn_positions_in_any_order():
+    # padding among the queries, a position twice, falling positions
+    K, V = pools(20, 16, 2, 128, torch.bfloat16, 5)
+    table = tables(2, 9, 20, 1).to(DEV)
+    g = torch.Generator().manual_seed(3)
+    t = torch.randint(-3, 150, (2, 50), generator=g)
+    t[0, 7], t[0, 8], t[1, 20:30] = 77, 77, -1
+    t = t.to(torch.int64).to(DEV)
+    q = randn((2, 50, 8, 128), 9).to(DEV)
+    for n_win, n_sink in ((0, 0), (20, 3)):
+        out, lse, _ = run_attn(q, K, V, table, t, n_win, n_sink)
+        check_attn(q, K, V, table, t, out, lse, 2.0 ** -8, n_win, n_sink)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attn_pages_shared_by_sequences(nq):
+    K, V = pools(9, 16, 2, 128, torch.bfloat16, 5)
+    table = torch.tensor([[1, 2, 3, 8], [1, 2, 5, 6], [1, 1, 1, 1]], dtype=torch.int32, device=DEV)
+    t = positions([64, 50, 41], nq).to(DEV)
+    q = randn((3, nq, 8, 128), 9).to(DEV)
+    out, lse, _ = run_attn(q, K, V, table, t)
+    check_attn(q, K, V, table, t, out, lse, weight_bits(nq, 8, 2, 128, torch.bfloat16, False))
+
+
+@pytest.mark.parametrize("nq,dtype", [(1, torch.bfloat16), (40, torch.bfloat16), (1, torch.float32)])
+def test_attn_status_of_an_uncleared_workspace(nq, dtype):
+    K, V = pools(9, 16, 2, 64, dtype, 5)
+    table = tables(2, 4, 9, 1).to(DEV)
+    q = randn((2, nq, 8, 64), 9, dtype).to(DEV)
+    ws = torch.full((lib.paged_attn_workspace_size(2, nq, 8, 2, 64, 64),), 0xff, dtype=torch.uint8, device=DEV)
+    lib.paged_attn(q, K, V, table, positions([60, 45], nq).to(DEV), torch.empty_like(q), ws)
+    assert lib.csa_workspace_status(ws) == 0
+
+
+def test_prompt_on_another_stream():
+    K, V = pools(9, 16, 2, 128, torch.bfloat16, 5)
+    table = tables(2, 4, 9, 1).to(DEV)
+    q = randn((2, 33, 8, 128), 9).to(DEV)
+    t = positions([60, 33], 33).to(DEV)
+    want = run_attn(q, K, V, table, t)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(q)
+    ws = torch.empty(lib.paged_attn_workspace_size(2, 33, 8, 2, 128, 64), dtype=torch.uint8, device=DEV)
+    with torch.cuda.stream(side):
+        lib.paged_attn(q, K, V, table, t, out, ws)
+    side.synchronize()
+    assert torch.equal(out, want[0])
+
+
+def test_two_prompts_at_once():
+    # two streams, each with its own workspace, many calls under way
+    K, V = pools(40, 16, 2, 128, torch.bfloat16, 5)
+    table = tables(2, 18, 40, 1).to(DEV)
+    qs = [randn((2, nq, 8, 128), 9 + nq).to(DEV) for nq in (70, 1)]
+    ts = [positions([280, 90], nq).to(DEV) for nq in (70, 1)]
+    want = [run_attn(q, K, V, table, t) for q, t in zip(qs, ts)]
+    streams = [torch.cuda.Stream() for _ in qs]
+    wss = [torch.empty(lib.paged_attn_workspace_size(2, q.shape[1], 8, 2, 128, 288), dtype=torch.uint8, device=DEV) for q in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, t, o, w, s in zip(qs, ts, outs, wss, streams):
+            lib.paged_attn(q, K, V, table, t, o, w, stream=s)
+    torch.cuda.synchronize()
+    for o, (x, _, _) in zip(outs, want):
+        assert torch.equal(o, x)
+
+
+@pytest.mark.parametrize("values", ["rand", "ties"])
+@pytest.mark.parametrize("B,n_kv,long,keep", [
+    (1, 160, 700, 300),    # more key heads than SMs: two selections an SM
+    (1, 150, 9000, 100),   # ... with runs that its registers do not hold
+    (1, 80, 17000, 5000),  # a CTA for each, too long for its registers
+    (1, 30, 9000, 3001),   # clusters of 4
+    (2, 15, 5000, 77),     # of 2
+])
+def test_evict_clusters(B, n_kv, long, keep, values):
+    evict_case([long, long // 2][:B], keep, 3, 20, n_kv=n_kv, d=8, page=64, values=values)
+
+
+def test_counts_that_do_not_fit_are_refused():
+    K, V = pools(4, 16, 2, 64, torch.bfloat16, 1)
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    t = torch.tensor([[5]], dtype=torch.int64, device=DEV)
+    q = randn((1, 1, 4, 64), 1).to(DEV)
+    out, ws = torch.empty_like(q), torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    for kw in (dict(n_win=2**32 + 4), dict(n_win=4, n_sink=2**31)):
+        with pytest.raises(ValueError):
+            lib.paged_attn(q, K, V, table, t, out, ws, **kw)
+    with pytest.raises(lib.CSAError):
+        lib.paged_attn(q, K, V, table, t, out, ws, n_win=-1)
