@@ -144,12 +144,14 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinColumns = 37;  // 32 x 37: every worker of a full GPU in one look
 
-// Pieces p0, p0 + step, ... of a row: their weighted sum, four under way at once.  slot(p): where piece p lies.
+// Pieces p0, p0 + step, ... of a row, four under way at once: their running maximum, sum and weighted sum.
+// slot(p): where piece p lies.
 template <int NC, typename F>
-CSA_DEV void join_pieces(const PagedAttnArgs& a, F slot, int p0, int step, int np, float M, float& L, float (&acc)[NC])
+CSA_DEV void join_pieces(const PagedAttnArgs& a, F slot, int p0, int step, int np, float& M, float& L, float (&acc)[NC])
 {
     constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31;
+    M = -INFINITY;
     L = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) acc[i] = 0.f;
@@ -161,17 +163,24 @@ CSA_DEV void join_pieces(const PagedAttnArgs& a, F slot, int p0, int step, int n
             const int64_t at = slot(min(p0 + k * step, np - 1));
             ml[k] = a.part_ml[at];
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (lane + 32 * i < a.d) v[k][i] = a.part_o[at * a.d + lane + 32 * i];
+            for (int i = 0; i < NC; ++i) v[k][i] = lane + 32 * i < a.d ? a.part_o[at * a.d + lane + 32 * i] : 0.f;
         }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (p0 + k * step < np) top = fmaxf(top, ml[k].x);
+        const float f = top == M ? 1.f : exp2f(M - top);
+        M = top;
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) acc[i] *= f;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const float w = p0 + k * step >= np || ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
             if (w == 0.f) continue;
             L = fmaf(w, ml[k].y, L);
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (lane + 32 * i < a.d) acc[i] = fmaf(w, v[k][i], acc[i]);
+            for (int i = 0; i < NC; ++i) acc[i] = fmaf(w, v[k][i], acc[i]);
         }
     }
 }
@@ -183,16 +192,17 @@ template <int NC>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs a)
 {
     constexpr int kMany = 16;  // pieces that a warp takes by itself: four rounds
-    __shared__ float sh[kJoinWarps];
+    __shared__ float2 sh[kJoinWarps];  // of a warp's pieces: maximum and sum
     __shared__ float so[kJoinWarps][NC * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, workers = a.runs * a.heads;
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) {
         int late = 0;
-        for (int i = lane; i < workers; i += 32) late |= a.desc[i].w;
-        late = __any_sync(0xffffffffu, late);
-        if (lane == 0) *a.status = late ? 1u : 0u;
+#pragma unroll 4
+        for (int i = tid; i < workers; i += kJoinThreads) late |= a.desc[i].w;
+        late = __syncthreads_or(late);
+        if (tid == 0) *a.status = late ? 1u : 0u;
     }
     for (int base = blockIdx.x; base < workers; base += 32 * gridDim.x) {
         const int mine = base + lane * gridDim.x;
@@ -212,12 +222,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
         int r;
         auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p * a.heads)) * a.R + r; };
         float M, L, acc[NC];
-        auto top = [&] {
-            M = -INFINITY;
-            for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
-#pragma unroll
-            for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        };
         auto store = [&] {
             const int64_t o = paged_out_row(a, b, tile, h, r);
             const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -229,19 +233,29 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
         for (unsigned todo = many; todo; todo &= todo - 1) {
             item(__ffs(todo) - 1);
             for (r = blockIdx.y; r < paged_rows(a, tile); r += gridDim.y) {
-                top();
                 join_pieces<NC>(a, slot, warp, kJoinWarps, np, M, L, acc);
                 __syncthreads();  // the row before
-                if (lane == 0) sh[warp] = L;
+                if (lane == 0) sh[warp] = make_float2(M, L);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) so[warp][lane + 32 * i] = acc[i];
                 __syncthreads();
                 if (warp > 0) continue;
+                float2 ml = lane < kJoinWarps ? sh[lane] : make_float2(-INFINITY, 0.f);
+                M = ml.x;
 #pragma unroll
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    L += sh[w];
+                for (int x = kJoinWarps / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                M = __shfl_sync(0xffffffffu, M, 0);
+                const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                L = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) acc[i] += so[w][lane + 32 * i];
+                for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    const float fw = __shfl_sync(0xffffffffu, f, w);
+                    if (fw == 0.f) continue;
+                    L = fmaf(fw, sh[w].y, L);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) acc[i] = fmaf(fw, so[w][lane + 32 * i], acc[i]);
                 }
                 store();
             }
@@ -252,7 +266,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
             item(__ffs(todo) - 1);
             for (; t < paged_rows(a, tile); t += gridDim.y * kJoinWarps) {
                 r = t;
-                top();
                 join_pieces<NC>(a, slot, 0, 1, np, M, L, acc);
                 store();
             }
