@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
 }
 
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinColumns = 37;  // 32 x 37: every worker of a full GPU in one look
 
 // Pieces p0, p0 + step, ... of a row, four under way at once: their running maximum, sum and weighted sum.
 // slot(p): where piece p lies.
@@ -468,13 +467,10 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
         st = sp.kind == kPagedPrompt ? launch_paged_prompt(a, sp, s) : launch_paged_decode(a, sp, s);
     }
     if (st != CSA_OK) return st;
-    // A decode call's rows are few and its items may have many pieces: a CTA for each row, an SM for each column (64
-    // windows of 1024 tokens: 64 us, 68 with the other grid).  A prompt's rows are many: one wave of three CTAs an SM (64
-    // rows of 16 sequences: 50 us, 57).  Nothing is cut into a single run, but the status is written.
-    const int rows = std::min(a.R, nq * G), workers = a.runs * a.heads;
-    const dim3 grid = a.runs == 1 ? dim3(1)
-                      : rows <= 16 ? dim3(std::min(workers, kNumSMs), rows)
-                                   : dim3(std::min(workers, kJoinColumns), 3 * kNumSMs / kJoinColumns);
+    // a CTA for each row of a decode call, eight rows of a prompt's tile for each CTA; nothing is cut into a single
+    // run, but the status is written
+    const int rows = std::min(a.R, nq * G), columns = std::min(a.runs * a.heads, kNumSMs);
+    const dim3 grid = a.runs == 1 ? dim3(1) : dim3(columns, std::min(rows, 32));
     if (d <= 128)
         launch_pdl(paged_attn_combine<4>, grid, dim3(kJoinThreads), 0, s, a);
     else

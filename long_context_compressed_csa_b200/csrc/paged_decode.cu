@@ -8,7 +8,7 @@
 //   bf16: the rows are the 16-row operand of mma.sync (m16n8k16), K is its B operand as stored,
 //         V through transposing ldmatrix.  The weights go to the second product as two bf16
 //         parts (hi + lo), which keeps 16 bits of them at the price of tensor work that is idle anyway.
-//         WR > 1: WR warps have 16 rows each and share a ring; they are one worker.
+//         WR > 1: WR warps have 16 rows each and share a ring; they are one worker, and round the weights once.
 //   fp32: plain FMAs, a token spread over LT lanes, RT rows in registers.
 #include "cluster.cuh"
 #include "paged.cuh"
@@ -110,7 +110,11 @@ struct MmaShape {
     static constexpr int kWarps = DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
     static constexpr int kGroups = kWarps / WR;                    // workers of a CTA
     static constexpr int kU = DP == 64 || (WR > 1 && DP == 128) ? 32 : 16;
-    static constexpr int kStages = WR == 4 ? 6 : 3;
+    static constexpr int kStages = DP == 256 && WR == 2 ? 2 : DP < 256 && WR == 4 ? 6 : 3;
+    static constexpr int kCtas = DP == 256 && WR > 1 ? 2 : 1;      // on an SM
+    // Many rows are bound by the tensor cores, not by the cache's bytes: the weights are rounded once then, as in
+    // the prompt kernel (half a step is 2^-9 to 2^-8 of a weight)
+    static constexpr bool kSplit = WR == 1;
     static constexpr int kRows = 16 * WR;
     static constexpr int kRing = kGroups * kStages * 2 * kU * DP * 2;    // bytes
     static constexpr int kQ = DP == 256 ? kGroups * kRows * DP * 2 : 0;  // wide heads: q in shared memory
@@ -118,7 +122,7 @@ struct MmaShape {
 };
 
 template <int DP, int WR>
-__global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, 1) paged_attn_mma(PagedAttnArgs a)
+__global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::kCtas) paged_attn_mma(PagedAttnArgs a)
 {
     using S = MmaShape<DP, WR>;
     constexpr int U = S::kU, R = S::kRows, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, 1) paged_attn_mma(
                 for (int x = 0; x < 4; ++x) {
                     const float p = s[t + (x >> 1)][2 * (x & 1)], p1 = s[t + (x >> 1)][2 * (x & 1) + 1];
                     hi[x] = pack2(p, p1);
-                    lo[x] = pack2(p - lo16(hi[x]), p1 - hi16(hi[x]));
+                    if (S::kSplit) lo[x] = pack2(p - lo16(hi[x]), p1 - hi16(hi[x]));
                 }
 #pragma unroll
                 for (int n = 0; n < DP / 8; n += 2) {
@@ -294,8 +298,10 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, 1) paged_attn_mma(
                     ldsm4_t(b, sv + at16<ROWB>(t * 8 + (lane & 15), n + (lane >> 4)));
                     mma16816(o[n], hi, b[0], b[1]);
                     mma16816(o[n + 1], hi, b[2], b[3]);
-                    mma16816(o[n], lo, b[0], b[1]);
-                    mma16816(o[n + 1], lo, b[2], b[3]);
+                    if constexpr (S::kSplit) {
+                        mma16816(o[n], lo, b[0], b[1]);
+                        mma16816(o[n + 1], lo, b[2], b[3]);
+                    }
                 }
             }
         }
@@ -581,7 +587,7 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
         // 19.4, 6 21.5, 8 24.0)
         s.min_units = 4;
         s.item_units = 4;
-        s.workers = (s.DP == 256 ? 4 : 8) / s.WR * kNumSMs;
+        s.workers = (s.DP == 256 && s.WR == 1 ? 4 : 8) / s.WR * kNumSMs;
     } else {
         s.kind = kPagedF32;
         s.WR = s.R = rows <= 4 ? 4 : 8;

@@ -60,8 +60,8 @@ def positions(lens, nq):
 
 def weight_bits(nq, n_h, n_kv, d, dtype, acc):
     """P of the module's bound: how exactly the call keeps the softmax weights (17 rows or more of a key
-    head take the kernel that rounds them once)."""
-    return 2.0 ** -8 if dtype == torch.bfloat16 and nq * n_h // n_kv >= 17 and d <= 128 else 2.0 ** -16
+    head take the kernels that round them once)."""
+    return 2.0 ** -8 if dtype == torch.bfloat16 and nq * n_h // n_kv >= 17 else 2.0 ** -16
 
 
 def check_attn(q, K, V, table, t, out, lse, P, n_win=0, n_sink=0, scale=None, acc=None, acc_out=None):
