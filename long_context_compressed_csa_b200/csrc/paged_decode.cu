@@ -107,8 +107,12 @@ struct Ring {
 
 template <int DP, int WR>
 struct MmaShape {
-    static constexpr int kWarps = DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
-    static constexpr int kGroups = kWarps / WR;                    // workers of a CTA
+    // Wide heads: two warps have the same 16 rows, both their logits and each half of the output columns, since a
+    // ring of 16 tokens is too large for eight groups and four warps do not hide their latencies
+    static constexpr int kWC = DP == 256 && WR == 1 ? 2 : 1;
+    static constexpr int kWarps = DP == 256 && WR > 1 ? 4 : 8, kThreads = 32 * kWarps;
+    static constexpr int kGW = WR * kWC;                           // warps of a group (a worker)
+    static constexpr int kGroups = kWarps / kGW;
     static constexpr int kU = DP == 64 || (WR > 1 && DP == 128) ? 32 : 16;
     static constexpr int kStages = DP == 256 && WR == 2 ? 2 : DP < 256 && WR == 4 ? 6 : 3;
     static constexpr int kCtas = DP == 256 && WR > 1 ? 2 : 1;      // on an SM
@@ -126,24 +130,26 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
 {
     using S = MmaShape<DP, WR>;
     constexpr int U = S::kU, R = S::kRows, NS = S::kStages, KS = DP / 16, NT = U / 8, ROWB = DP * 2;
+    constexpr int WC = S::kWC, GW = S::kGW, ON = DP / 8 / WC;  // ON: output tiles of 8 columns of a warp
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ PagedScratch<S::kThreads, 1> sh;
     __shared__ uint32_t masks[S::kGroups * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = warp / WR, wr = warp % WR, worker = blockIdx.x * S::kGroups + group;
+    const int group = warp / GW, wr = warp % GW / WC, wc = warp % WC, worker = blockIdx.x * S::kGroups + group;
+    const bool first = warp % GW == 0 && lane == 0;  // of the worker's threads
     const int run = worker / a.heads;
     uint8_t* sring = smem + S::kQ;
     pdl_launch_dependents();
     pdl_wait();
-    if (run < a.runs && wr == 0 && lane == 0) a.desc[worker] = make_int4(-1, 0, 0, 0);
+    if (run < a.runs && first) a.desc[worker] = make_int4(-1, 0, 0, 0);
     PagedCursor c;
     if (!paged_schedule<S::kThreads, 1, true>(a, run, sh, c)) return;
     c.h = worker - run * a.heads;
-    Ring<ROWB, U, WR> ring;
+    Ring<ROWB, U, GW> ring;
     ring.base = tc::smem_u32(sring) + group * (NS * ring.kStage);
     ring.masks = masks + group * NS;
     ring.row_bytes = a.d * 2;
-    ring.lane = wr * 32 + lane;
+    ring.lane = warp % GW * 32 + lane;
     ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
     ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
     while (true) {
         const PagedSegment sg = paged_segment(a, c, worker);
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
-        if (wr == 0 && lane == 0) paged_describe(a, c, sg, worker);
+        if (first) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
         const int n_u = sg.u1 - sg.u0;
 #pragma unroll
@@ -163,14 +169,14 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
         }
         uint32_t qf[DP == 256 ? 1 : KS][4];
         if constexpr (DP == 256) {
-            for (int x = lane; x < 16 * (DP / 8); x += 32) {
+            for (int x = wc * 32 + lane; x < 16 * (DP / 8); x += 32 * WC) {
                 const int r = x / (DP / 8), ch = x % (DP / 8);
                 const int64_t o = paged_out_row(a, en.b, en.tile, c.h, wr * 16 + r);
                 const bool in = o >= 0 && ch * 8 < a.d;
                 const uint4 v = in ? *reinterpret_cast<const uint4*>(q + o * a.d + ch * 8) : make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4*>(my_q + at16<ROWB>(r, ch)) = v;
             }
-            __syncwarp();
+            group_sync<GW>(group);
         } else {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -193,20 +199,20 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
             const int row = en.tile * R + r0 + 8 * half;
             row_in[half] = row < a.nq * a.G;
             rb[half] = row_in[half] ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
-            lg[half] = a.logits && row_in[half]
+            lg[half] = a.logits && row_in[half] && wc == 0
                            ? a.logits + (((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap
                            : nullptr;
         }
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[DP / 8][4];
+        float o[ON][4];
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i)
+        for (int i = 0; i < ON; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
         int st = 0;
         for (int i = 0; i < n_u; ++i) {
             cp_wait<NS - 2>();
-            group_sync<WR>(group);
+            group_sync<GW>(group);
             const int u = sg.u0 + i;
             {
                 const int nx = st == 0 ? NS - 1 : st - 1;
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
             }
             if (__any_sync(0xffffffffu, shrink[0] != 1.f || shrink[1] != 1.f)) {
 #pragma unroll
-                for (int i2 = 0; i2 < DP / 8; ++i2)
+                for (int i2 = 0; i2 < ON; ++i2)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[i2][x] *= shrink[x >> 1];
             }
@@ -293,9 +299,9 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
                     if (S::kSplit) lo[x] = pack2(p - lo16(hi[x]), p1 - hi16(hi[x]));
                 }
 #pragma unroll
-                for (int n = 0; n < DP / 8; n += 2) {
-                    uint32_t b[4];  // tokens t*8 .. +15, columns n*8 .. +15: {k0 n0, k8 n0, k0 n8, k8 n8}
-                    ldsm4_t(b, sv + at16<ROWB>(t * 8 + (lane & 15), n + (lane >> 4)));
+                for (int n = 0; n < ON; n += 2) {
+                    uint32_t b[4];  // tokens t*8 .. +15, 16 columns: {k0 n0, k8 n0, k0 n8, k8 n8}
+                    ldsm4_t(b, sv + at16<ROWB>(t * 8 + (lane & 15), wc * ON + n + (lane >> 4)));
                     mma16816(o[n], hi, b[0], b[1]);
                     mma16816(o[n + 1], hi, b[2], b[3]);
                     if constexpr (S::kSplit) {
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
             }
         }
         cp_wait<0>();
-        group_sync<WR>(group);  // the ring is filled anew
+        group_sync<GW>(group);  // the ring is filled anew
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = r0 + 8 * half;
@@ -317,8 +323,8 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
                 const int64_t at = paged_out_row(a, en.b, en.tile, c.h, r);
                 const float inv = l[half] == 0.f ? 0.f : 1.f / l[half];
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n) {
-                    const int col = n * 8 + 2 * (lane & 3);
+                for (int n = 0; n < ON; ++n) {
+                    const int col = (wc * ON + n) * 8 + 2 * (lane & 3);
                     const float x = o[n][2 * half] * inv, y = o[n][2 * half + 1] * inv;
                     if (col >= a.d) continue;
                     if (a.out_bf16)
@@ -326,17 +332,17 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
                     else
                         *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at * a.d + col) = make_float2(x, y);
                 }
-                if ((lane & 3) == 0) paged_store_lse(a, at, en.b, en.tile, c.h, r, m[half], l[half]);
+                if ((lane & 3) == 0 && wc == 0) paged_store_lse(a, at, en.b, en.tile, c.h, r, m[half], l[half]);
             } else {
                 const int64_t at = (int64_t)sg.slot * R + r;
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n) {
-                    const int col = n * 8 + 2 * (lane & 3);
+                for (int n = 0; n < ON; ++n) {
+                    const int col = (wc * ON + n) * 8 + 2 * (lane & 3);
                     if (col < a.d)
                         *reinterpret_cast<float2*>(a.part_o + at * a.d + col) =
                             make_float2(o[n][2 * half], o[n][2 * half + 1]);
                 }
-                if ((lane & 3) == 0) a.part_ml[at] = make_float2(m[half], l[half]);
+                if ((lane & 3) == 0 && wc == 0) a.part_ml[at] = make_float2(m[half], l[half]);
             }
         }
         if (!paged_next<1, true>(a, c, sg)) break;
