@@ -340,7 +340,7 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
 }
 
 // Which kernel a call runs on, its row tile, and the units and CTAs of its schedule.
-enum PagedKind { kPagedSimt, kPagedMma, kPagedF32, kPagedPrompt };
+enum PagedKind { kPagedSimt, kPagedFew, kPagedMma, kPagedF32, kPagedPrompt };
 struct PagedShape {
     PagedKind kind;
     int DP;         // head width rounded up to a kernel's

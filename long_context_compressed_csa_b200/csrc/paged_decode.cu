@@ -78,21 +78,39 @@ struct Ring {
     uint32_t* masks;        // [stages]: bit r of a word: row r has a token
     const char *K, *V;      // of this key head
     int row_bytes;          // d elements
+    bool one_page;          // a unit never lies in two pages
     int lane;               // within the group
 
     // Start of the loads of unit u into `stage`; every lane of the group.
     CSA_DEV void load(const PagedAttnArgs& a, const PagedEntry& en, int u, int stage, int eb)
     {
         const int j0 = en.first_token(u, U), l = lane & 31;
+        const uint32_t s = base + stage * kStage;
+        // a pass takes kLanes chunks: kLanes / kChunks rows, or a part of one row
+        constexpr int kPasses = U * kChunks / kLanes;
+        static_assert(U * kChunks % kLanes == 0, "whole passes");
+        // Nearly every unit lies in one page and is wholly visible to some row: one look at the table, and rows
+        // at a fixed distance (a third of the instructions of the way below).
+        if (one_page && j0 >= en.lo_min && j0 + U <= en.hi_max) {
+            const int64_t first = paged_row(a.pl, en.b, j0);
+            if (first >= 0) {
+                if (lane == 0) masks[stage] = U == 32 ? ~0u : (1u << (U & 31)) - 1;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int x = i * kLanes + lane, r = x / kChunks, c = x % kChunks;
+                    const bool take = c * 16 < row_bytes;
+                    const int64_t at = take ? (first + r * a.pl.ld_row) * eb + c * 16 : 0;
+                    cp16(s + at16<ROWB>(r, c), K + at, take);
+                    cp16(s + U * ROWB + at16<ROWB>(r, c), V + at, take);
+                }
+                return;
+            }
+        }
         int64_t off = -1;
         if (l < U && j0 + l < a.cap && en.seen(j0 + l)) off = paged_row(a.pl, en.b, j0 + l);
         const unsigned have = __ballot_sync(0xffffffffu, off >= 0);
         if (lane == 0) masks[stage] = have;
         off *= eb;
-        const uint32_t s = base + stage * kStage;
-        // a pass takes kLanes chunks: kLanes / kChunks rows, or a part of one row
-        constexpr int kPasses = U * kChunks / kLanes;
-        static_assert(U * kChunks % kLanes == 0, "whole passes");
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int x = i * kLanes + lane, r = x / kChunks, c = x % kChunks;
@@ -149,6 +167,7 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
     ring.base = tc::smem_u32(sring) + group * (NS * ring.kStage);
     ring.masks = masks + group * NS;
     ring.row_bytes = a.d * 2;
+    ring.one_page = a.pl.page % U == 0;
     ring.lane = warp % GW * 32 + lane;
     ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
     ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
@@ -349,6 +368,211 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
     }
 }
 
+// The two 8 x 8 blocks of 16-bit values of a fragment, transposed.
+CSA_DEV uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int DP>
+struct FewShape {
+    static constexpr int kU = DP == 64 ? 32 : 16, kStages = 3, kRows = 8;
+    static constexpr int kWC = DP == 256 ? 2 : 1;                  // warps of a worker, each half of the columns
+    static constexpr int kWarps = 8, kThreads = 32 * kWarps, kGroups = kWarps / kWC;
+    static constexpr int kSmem = kGroups * kStages * 2 * kU * DP * 2;
+};
+
+// Eight rows or fewer (a decode step of most head layouts): the products the other way round, so that the rows are
+// the 8-wide side of m16n8k16 and no row of it is padding:
+//   S^T (16 tokens x 8 rows) = K Q^T,   O^T (16 columns x 8 rows) += V^T P^T.
+// A lane has two rows (2 (lane mod 4) and the next) and tokens, or columns, lane / 4 and 8 more.  P^T becomes the
+// second product's operand by a transposition of its 8 x 8 blocks.  Half the tensor work and half the logits a
+// lane of the 16-row kernel, whose time and power (not the cache's bytes alone) bounded long decodes.
+template <int DP>
+__global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(PagedAttnArgs a)
+{
+    using S = FewShape<DP>;
+    constexpr int U = S::kU, NS = S::kStages, KS = DP / 16, NT = U / 16, ROWB = DP * 2, WC = S::kWC, ON = DP / 16 / WC;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ PagedScratch<S::kThreads, 1> sh;
+    __shared__ uint32_t masks[S::kGroups * NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = warp / WC, wc = warp % WC, worker = blockIdx.x * S::kGroups + group;
+    const int run = worker / a.heads;
+    const bool first = wc == 0 && lane == 0;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (run < a.runs && first) a.desc[worker] = make_int4(-1, 0, 0, 0);
+    PagedCursor c;
+    if (!paged_schedule<S::kThreads, 1, true>(a, run, sh, c)) return;
+    c.h = worker - run * a.heads;
+    Ring<ROWB, U, WC> ring;
+    ring.base = tc::smem_u32(smem) + group * (NS * ring.kStage);
+    ring.masks = masks + group * NS;
+    ring.row_bytes = a.d * 2;
+    ring.one_page = a.pl.page % U == 0;
+    ring.lane = wc * 32 + lane;
+    ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 2;
+    ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 2;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    const int r0 = 2 * (lane & 3), k0 = lane >> 2;  // this lane's first row; its token, or column, of a block
+    while (true) {
+        const PagedSegment sg = paged_segment(a, c, worker);
+        if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
+        if (first) paged_describe(a, c, sg, worker);
+        const PagedEntry en = c.en;
+        const int n_u = sg.u1 - sg.u0;
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) {
+            if (s < n_u) ring.load(a, en, sg.u0 + s, s, 2);
+            cp_commit();
+        }
+        uint32_t qf[KS][2];
+        {
+            const int64_t o = paged_out_row(a, en.b, en.tile, c.h, k0);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int col = k * 16 + p * 8 + 2 * (lane & 3);
+                    qf[k][p] = o >= 0 && col < a.d ? *reinterpret_cast<const uint32_t*>(q + o * a.d + col) : 0u;
+                }
+        }
+        RowBounds rb[2];
+        bool row_in[2];
+        float* lg[2];  // the rows' logits, when they are asked for
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int row = en.tile * S::kRows + r0 + x;
+            row_in[x] = row < a.nq * a.G;
+            rb[x] = row_in[x] ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
+            lg[x] = a.logits && row_in[x] && wc == 0
+                        ? a.logits + (((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap
+                        : nullptr;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[ON][4];
+#pragma unroll
+        for (int i = 0; i < ON; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+        int st = 0;
+        for (int i = 0; i < n_u; ++i) {
+            cp_wait<NS - 2>();
+            group_sync<WC>(group);
+            const int u = sg.u0 + i;
+            {
+                const int nx = st == 0 ? NS - 1 : st - 1;
+                if (i + NS - 1 < n_u) ring.load(a, en, u + NS - 1, nx, 2);
+                cp_commit();
+            }
+            const uint32_t sk = ring.base + st * ring.kStage, sv = sk + U * ROWB;
+            const unsigned have = ring.masks[st];
+            st = st == NS - 1 ? 0 : st + 1;
+            // two partial sums a tile: a chain of KS products is the longest wait of a unit
+            float s[NT][4], s2[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[t][x] = s2[t][x] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; k += 2)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint32_t f[4];  // tokens t*16 .. +15, k16 step: {m0 k0, m8 k0, m0 k8, m8 k8}
+                    ldsm4(f, sk + at16<ROWB>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
+                    mma16816(s[t], f, qf[k][0], qf[k][1]);
+                    ldsm4(f, sk + at16<ROWB>(t * 16 + (lane & 15), 2 * k + 2 + (lane >> 4)));
+                    mma16816(s2[t], f, qf[k + 1][0], qf[k + 1][1]);
+                }
+            const int j0 = en.first_token(u, U);
+            const bool clear = j0 >= en.lo_max && j0 + U <= en.hi_min && have == (U == 32 ? ~0u : (1u << (U & 31)) - 1);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int r = t * 16 + k0 + 8 * (x >> 1);
+                    float v = (s[t][x] + s2[t][x]) * a.scale_log2;
+                    if (!clear && !((have >> r & 1) && paged_visible(rb[x & 1], j0 + r))) v = -INFINITY;
+                    s[t][x] = v;
+                    top[x & 1] = fmaxf(top[x & 1], v);
+                    if (a.logits && lg[x & 1] && j0 + r < a.cap) lg[x & 1][j0 + r] = v;
+                }
+            float shrink[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], y));
+                const float mn = fmaxf(m[x], top[x]);
+                shrink[x] = mn == m[x] ? 1.f : tc::ex2_approx(m[x] - mn);  // m = -inf: 0
+                m[x] = mn;
+                l[x] *= shrink[x];
+            }
+            if (__any_sync(0xffffffffu, shrink[0] != 1.f || shrink[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < ON; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[n][x] *= shrink[x & 1];
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p = tc::ex2_approx(s[t][2 * x] - base[0]), p1 = tc::ex2_approx(s[t][2 * x + 1] - base[1]);
+                    l[0] += p;
+                    l[1] += p1;
+                    hi[x] = pack2(p, p1);
+                    lo[x] = transpose8(pack2(p - lo16(hi[x]), p1 - hi16(hi[x])));
+                    hi[x] = transpose8(hi[x]);
+                }
+#pragma unroll
+                for (int n = 0; n < ON; ++n) {
+                    uint32_t f[4];  // columns n*16 .. +15, tokens t*16 .. +15: {m0 k0, m8 k0, m0 k8, m8 k8}
+                    ldsm4_t(f, sv + at16<ROWB>(t * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                               2 * (wc * ON + n) + ((lane >> 3) & 1)));
+                    mma16816(o[n], f, hi[0], hi[1]);
+                    mma16816(o[n], f, lo[0], lo[1]);
+                }
+            }
+        }
+        cp_wait<0>();
+        group_sync<WC>(group);  // the ring is filled anew
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], y);
+            if (!row_in[x]) continue;
+            const int64_t at = sg.whole ? paged_out_row(a, en.b, en.tile, c.h, r0 + x) : (int64_t)sg.slot * S::kRows + r0 + x;
+            const float inv = sg.whole ? (l[x] == 0.f ? 0.f : 1.f / l[x]) : 1.f;
+#pragma unroll
+            for (int n = 0; n < ON; ++n)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int col = (wc * ON + n) * 16 + 8 * y + k0;
+                    const float v = o[n][2 * y + x] * inv;
+                    if (col >= a.d) continue;
+                    if (sg.whole)
+                        paged_store(a, at * a.d + col, v);
+                    else
+                        a.part_o[at * a.d + col] = v;
+                }
+            if (k0 == 0 && wc == 0) {
+                if (sg.whole)
+                    paged_store_lse(a, at, en.b, en.tile, c.h, r0 + x, m[x], l[x]);
+                else
+                    a.part_ml[at] = make_float2(m[x], l[x]);
+            }
+        }
+        __syncwarp();
+        if (!paged_next<1, true>(a, c, sg)) break;
+    }
+}
+
 template <int DP, int RT>
 struct F32Shape {
     static constexpr int kEL = 64 / RT;      // elements of a row that a lane has
@@ -381,6 +605,7 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
     ring.base = tc::smem_u32(smem) + warp * (NS * ring.kStage);
     ring.masks = masks + warp * NS;
     ring.row_bytes = a.d * 4;
+    ring.one_page = a.pl.page % U == 0;
     ring.lane = lane;
     ring.K = static_cast<const char*>(a.K) + c.h * a.pl.ld_head * 4;
     ring.V = static_cast<const char*>(a.V) + c.h * a.pl.ld_head * 4;
@@ -569,6 +794,12 @@ int launch_mma(const PagedAttnArgs& a, cudaStream_t stream)
     using S = MmaShape<DP, WR>;
     return launch(paged_attn_mma<DP, WR>, S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
+template <int DP>
+int launch_few(const PagedAttnArgs& a, cudaStream_t stream)
+{
+    using S = FewShape<DP>;
+    return launch(paged_attn_few<DP>, S::kThreads, S::kGroups, S::kSmem, a, stream);
+}
 template <int DP, int RT>
 int launch_f32(const PagedAttnArgs& a, cudaStream_t stream)
 {
@@ -584,7 +815,14 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
     PagedShape s{};
     s.DP = d <= 64 ? 64 : d <= 128 ? 128 : 256;
     s.by_head = true;
-    if (dtype == CSA_BF16) {
+    if (dtype == CSA_BF16 && rows <= 8) {
+        s.kind = kPagedFew;
+        s.R = 8;
+        s.unit = s.DP == 64 ? 32 : 16;
+        s.min_units = 4;  // as below
+        s.item_units = 4;
+        s.workers = (s.DP == 256 ? 4 : 8) * kNumSMs;
+    } else if (dtype == CSA_BF16) {
         s.kind = kPagedMma;
         s.WR = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         s.R = 16 * s.WR;
@@ -607,6 +845,8 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
 
 int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream)
 {
+    if (s.kind == kPagedFew)
+        return s.DP == 64 ? launch_few<64>(a, stream) : s.DP == 128 ? launch_few<128>(a, stream) : launch_few<256>(a, stream);
     if (s.kind == kPagedF32) {
         if (s.DP == 64) return s.WR == 4 ? launch_f32<64, 4>(a, stream) : launch_f32<64, 8>(a, stream);
         if (s.DP == 128) return s.WR == 4 ? launch_f32<128, 4>(a, stream) : launch_f32<128, 8>(a, stream);
