@@ -499,8 +499,16 @@ __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(Page
                     if (!clear && !((have >> r & 1) && paged_visible(rb[x & 1], j0 + r))) v = -INFINITY;
                     s[t][x] = v;
                     top[x & 1] = fmaxf(top[x & 1], v);
-                    if (a.logits && lg[x & 1] && j0 + r < a.cap) lg[x & 1][j0 + r] = v;
                 }
+            if (a.logits) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int j = j0 + t * 16 + k0 + 8 * (x >> 1);
+                        if (lg[x & 1] && j < a.cap) lg[x & 1][j] = s[t][x];
+                    }
+            }
             float shrink[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
