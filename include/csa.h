@@ -389,8 +389,12 @@ int hca_dense_attn_window(const void* q, const void* cache, const int64_t* t, co
  * t      : int64 [B, nq] (device): the cache position of each new token; t < 0 marks
  *          padding.  Positions count cached tokens, so after paged_evict they go on
  *          from the new length.
- * Constraints: 1 <= d <= 256 (paged_attn), cap < 2^31 - 1024.  Rows that no visible token has may hold
- * anything, NaN included.
+ * Constraints: 1 <= d <= 256 (paged_attn), cap < 2^31 - 1024.  Rows that no query of a call sees may hold
+ * anything, NaN included: they reach no result.  A NaN or an infinity in a row that some query sees may reach all
+ * queries of the same sequence and key head in that call.
+ * Layouts: any alignment of whole elements is right; rows that start on 16 bytes and are whole 16-byte words are
+ * what the fast kernels take, and a prompt (17 packed rows nq * G or more, bf16, d <= 128) also wants pages
+ * of a multiple of 8 rows.
  * ------------------------------------------------------------------------------- */
 
 /* paged_append - writes the keys and values of new tokens into their pages: token i of sequence b
@@ -416,9 +420,13 @@ int paged_append(const void* k, const void* v, int64_t ld_batch, int64_t ld_tok,
  * acc, acc_out : both NULL, or fp32 [B, n_kv, cap]: acc_out[b][h][j] = acc[b][h][j] + the
  *          attention weight that token j got from all queries and query heads of key head h.  They may
  *          be the same buffer; every element of acc_out is written.
- * A query that sees nothing gets out = 0 and lse = -inf.
+ * A query that sees nothing gets out = 0 and lse = -inf.  A logit of NaN makes its row's out and lse NaN.
+ * Logits, running maxima, sums and outputs are fp32.  bf16: the softmax weights go to the second product in two
+ * bf16 parts (16 bits of them), in one (8 bits) with 17 packed rows nq * G or more, where that product
+ * bounds the call; the row sums take them before the rounding.  Results do not change from run to run.
  * workspace : >= paged_attn_workspace_size(...) bytes, 16-byte aligned; weights != 0 when acc is
- *          given.  Its contents need not be set and mean nothing between calls.
+ *          given.  Its contents need not be set and mean nothing between calls, but for the status word that
+ *          every call writes (csa_workspace_status).  Calls that may overlap need one each.
  * The lengths are read on the device: a captured call follows t and table. */
 size_t paged_attn_workspace_size(int B, int nq, int n_h, int n_kv, int d, int64_t cap, int weights);
 int paged_attn(const void* q, const void* K, const void* V, int64_t pool_ld_page, int64_t pool_ld_row,
@@ -446,10 +454,11 @@ int paged_evict(void* K, void* V, int64_t pool_ld_page, int64_t pool_ld_row, int
                 const int32_t* new_table, int new_max_pages, int64_t* new_lens, float* new_acc,
                 int32_t* idx_out, int dtype, csa_stream_t stream);
 
-/* Device status of a workspace of csa_indexer_topk, csa_sparse_attn or hca_dense_attn:
+/* Device status of a workspace of csa_indexer_topk, csa_sparse_attn, hca_dense_attn or paged_attn:
  * synchronises `stream` and returns CSA_OK, or CSA_ERR_TIMEOUT if a tensor-core kernel
  * of an earlier call gave up a bounded wait (its outputs are then invalid).  The status
- * word is the first 4 bytes of the workspace and stays set until it is zeroed. */
+ * word is the first 4 bytes of the workspace and stays set until it is zeroed (paged_attn: until the
+ * next call with that workspace, which writes its own). */
 int csa_workspace_status(const void* workspace, csa_stream_t stream);
 
 /* Test hook of the failure detection (no counterpart in the pages): sets, on `stream`,

@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
     __shared__ PagedScratch<S::kThreads, 1> sh;
     __shared__ uint32_t masks[S::kGroups * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = warp / GW, wr = warp % GW / WC, wc = warp % WC, worker = blockIdx.x * S::kGroups + group;
+    const int group = warp / GW, wr = warp % GW / WC, wc = warp % WC, worker = blockIdx.x * a.per_cta + group;
     const bool first = warp % GW == 0 && lane == 0;  // of the worker's threads
-    const int run = worker / a.heads;
+    const int run = group < a.per_cta ? worker / a.heads : a.runs;  // a.runs: none
     uint8_t* sring = smem + S::kQ;
     pdl_launch_dependents();
     pdl_wait();
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(Page
     __shared__ PagedScratch<S::kThreads, 1> sh;
     __shared__ uint32_t masks[S::kGroups * NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = warp / WC, wc = warp % WC, worker = blockIdx.x * S::kGroups + group;
-    const int run = worker / a.heads;
+    const int group = warp / WC, wc = warp % WC, worker = blockIdx.x * a.per_cta + group;
+    const int run = group < a.per_cta ? worker / a.heads : a.runs;  // a.runs: none
     const bool first = wc == 0 && lane == 0;
     pdl_launch_dependents();
     pdl_wait();
@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ PagedScratch<S::kThreads, 1> sh;
     __shared__ uint32_t masks[S::kWarps * NS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, worker = blockIdx.x * S::kWarps + warp;
-    const int run = worker / a.heads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, worker = blockIdx.x * a.per_cta + warp;
+    const int run = warp < a.per_cta ? worker / a.heads : a.runs;  // a.runs: none
     const int g = lane / LT, e = lane % LT;
     pdl_launch_dependents();
     pdl_wait();
@@ -785,14 +785,18 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
 }
 
 template <typename F>
-int launch(F* kern, int threads, int workers, int smem, const PagedAttnArgs& a, cudaStream_t stream)
+int launch(F* kern, int threads, int groups, int smem, PagedAttnArgs a, cudaStream_t stream)
 {
+    // few workers: one or two on every SM, not eight on a few
+    const int workers = a.runs * a.heads;
+    a.per_cta = (workers + kNumSMs - 1) / kNumSMs;
+    if (a.per_cta > groups) a.per_cta = groups;
     // per device and idempotent; no state is kept between calls
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return CSA_ERR_CUDA;
     }
-    launch_pdl(kern, dim3((a.runs * a.heads + workers - 1) / workers), dim3(threads), smem, stream, a);
+    launch_pdl(kern, dim3((workers + a.per_cta - 1) / a.per_cta), dim3(threads), smem, stream, a);
     return launch_status();
 }
 
