@@ -9,7 +9,7 @@
 //         V through transposing ldmatrix.  The weights go to the second product as two bf16
 //         parts (hi + lo), which keeps 16 bits of them at the price of tensor work that is idle anyway.
 //         WR > 1: WR warps have 16 rows each and share a ring; they are one worker, and round the weights once.
-//   fp32: plain FMAs, a token spread over LT lanes, RT rows in registers.
+//   fp32: packed FMAs, a token spread over LT lanes, RT rows in registers.
 #include "cluster.cuh"
 #include "paged.cuh"
 #include "tc_utils.cuh"
@@ -597,9 +597,13 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
 {
     using S = F32Shape<DP, RT>;
     constexpr int U = S::kU, NS = S::kStages, EL = S::kEL, LT = S::kLT, NG = S::kNG, TG = U / NG, ROWB = DP * 4;
+    // N logits of a token group at a time; NV of them a lane, or SH lanes with the same one
+    constexpr int N = TG * RT, NV = N > LT ? N / LT : 1, SH = LT > N ? LT / N : 1;
+    static_assert(RT % NV == 0 && TG * NG == U, "a lane's logits are of one token");
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ PagedScratch<S::kThreads, 1> sh;
     __shared__ uint32_t masks[S::kWarps * NS];
+    __shared__ RowBounds bounds[S::kWarps][RT];  // of the rows of each warp's item
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, worker = blockIdx.x * a.per_cta + warp;
     const int run = warp < a.per_cta ? worker / a.heads : a.runs;  // a.runs: none
     const int g = lane / LT, e = lane % LT;
@@ -630,13 +634,22 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
             if (s < n_u) ring.load(a, en, sg.u0 + s, s, 4);
             cp_commit();
         }
+        __syncwarp();
+        if (lane < RT) {
+            const int row = en.tile * RT + lane;
+            bounds[warp][lane] = row < a.nq * a.G ? paged_bounds(a, en.b, row / a.G) : RowBounds{0, 0, 0};
+        }
+        __syncwarp();
         float2 qr[RT][EL / 2], o[RT][EL / 2];
-        float m[RT], l[RT];
+        float m_own[NV], l_own[NV];  // of this lane's rows
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            m_own[i] = -INFINITY;
+            l_own[i] = 0.f;
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int64_t at = paged_out_row(a, en.b, en.tile, c.h, r);
-            m[r] = -INFINITY;
-            l[r] = 0.f;
 #pragma unroll
             for (int x = 0; x < EL / 2; ++x) {
                 const int col = (e + LT * (x / 2)) * 4 + 2 * (x & 1);
@@ -662,11 +675,12 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
             st = st == NS - 1 ? 0 : st + 1;
             const int j0 = en.first_token(u, U);
             const bool clear = j0 >= en.lo_max && j0 + U <= en.hi_min && have == (U == 32 ? ~0u : (1u << (U & 31)) - 1);
-            float s[TG][RT];
+            // this lane's part of the N logits of its token group, (token, row) in the order token * RT + row
+            float s[N];
 #pragma unroll
             for (int t = 0; t < TG; ++t) {
                 const int r8 = t * NG + g;
-                float2 k[EL / 2], dot[RT];
+                float2 k[EL / 2];
 #pragma unroll
                 for (int x = 0; x < EL / 4; ++x) {
                     const float4 v = *reinterpret_cast<const float4*>(sk + at16<ROWB>(r8, e + LT * x));
@@ -675,65 +689,77 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
                 }
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    dot[r] = make_float2(0.f, 0.f);
+                    float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int x = 0; x < EL / 2; ++x) dot[r] = tc::fma2(qr[r][x], k[x], dot[r]);
-                    s[t][r] = dot[r].x + dot[r].y;
-#pragma unroll
-                    for (int y = LT / 2; y; y >>= 1) s[t][r] += __shfl_xor_sync(0xffffffffu, s[t][r], y);
-                    s[t][r] *= a.scale_log2;
-                }
-                if (!clear) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const int row = en.tile * RT + r;
-                        if (!((have >> r8 & 1) && row < a.nq * a.G &&
-                              paged_visible(paged_bounds(a, en.b, row / a.G), j0 + r8)))
-                            s[t][r] = -INFINITY;
-                    }
-                }
-                if (a.logits && e == 0 && j0 + r8 < a.cap) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const int row = en.tile * RT + r;
-                        if (row < a.nq * a.G)
-                            a.logits[(((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap + j0 + r8] = s[t][r];
-                    }
+                    for (int x = 0; x < EL / 2; ++x) dot = tc::fma2(qr[r][x], k[x], dot);
+                    s[t * RT + r] = dot.x + dot.y;
                 }
             }
+            // Summed over the LT lanes so that each ends with NV whole logits: in a step a lane keeps half of its
+            // values and hands the other half to its partner (30 shuffles for 32 logits instead of 128)
+            int n = N;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float mn = m[r];
+            for (int y = LT / 2; y; y >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+                    const bool up = e & y;
 #pragma unroll
-                for (int t = 0; t < TG; ++t) mn = fmaxf(mn, s[t][r]);
-                if (mn != m[r]) {
-                    const float f = tc::ex2_approx(m[r] - mn);
-                    m[r] = mn;
-                    l[r] *= f;
+                    for (int x = 0; x < N / 2; ++x)
+                        if (x < n) {
+                            const float keep = up ? s[x + n] : s[x], give = up ? s[x] : s[x + n];
+                            s[x] = keep + __shfl_xor_sync(0xffffffffu, give, y);
+                        }
+                } else {
+                    s[0] += __shfl_xor_sync(0xffffffffu, s[0], y);
+                }
+            }
+            float shrink[NV];
+            bool grew = false;
+#pragma unroll
+            for (int x = 0; x < NV; ++x) {
+                const int at = e / SH * NV + x, r = at % RT, r8 = at / RT * NG + g;
+                s[x] *= a.scale_log2;
+                if (!clear && !((have >> r8 & 1) && paged_visible(bounds[warp][r], j0 + r8))) s[x] = -INFINITY;
+                const int row = en.tile * RT + r;
+                if (a.logits && e % SH == 0 && j0 + r8 < a.cap && row < a.nq * a.G)
+                    a.logits[(((int64_t)en.b * a.n_kv + c.h) * (a.nq * a.G) + row) * a.cap + j0 + r8] = s[x];
+                float top = s[x];  // over the tokens of the row
+#pragma unroll
+                for (int y = RT * SH / NV; y < LT; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+                const float mn = fmaxf(m_own[x], top);
+                shrink[x] = mn == m_own[x] ? 1.f : tc::ex2_approx(m_own[x] - mn);
+                grew |= shrink[x] != 1.f;
+                m_own[x] = mn;
+                s[x] = tc::ex2_approx(s[x] - (mn == -INFINITY ? 0.f : mn));
+                l_own[x] = l_own[x] * shrink[x] + s[x];
+            }
+            const int lane0 = lane - e;  // of the token group
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, shrink[r % NV], lane0 + r / NV * SH);
 #pragma unroll
                     for (int x = 0; x < EL / 2; ++x) {
                         o[r][x].x *= f;
                         o[r][x].y *= f;
                     }
                 }
-                const float base = mn == -INFINITY ? 0.f : mn;
-#pragma unroll
-                for (int t = 0; t < TG; ++t) {
-                    s[t][r] = tc::ex2_approx(s[t][r] - base);
-                    l[r] += s[t][r];
-                }
             }
 #pragma unroll
             for (int t = 0; t < TG; ++t) {
                 const int r8 = t * NG + g;
+                float4 v[EL / 4];
 #pragma unroll
-                for (int x = 0; x < EL / 4; ++x) {
-                    const float4 v = *reinterpret_cast<const float4*>(sv + at16<ROWB>(r8, e + LT * x));
+                for (int x = 0; x < EL / 4; ++x) v[x] = *reinterpret_cast<const float4*>(sv + at16<ROWB>(r8, e + LT * x));
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const float2 p = make_float2(s[t][r], s[t][r]);
-                        o[r][2 * x] = tc::fma2(p, make_float2(v.x, v.y), o[r][2 * x]);
-                        o[r][2 * x + 1] = tc::fma2(p, make_float2(v.z, v.w), o[r][2 * x + 1]);
+                for (int r = 0; r < RT; ++r) {
+                    const int at = t * RT + r;
+                    const float w = __shfl_sync(0xffffffffu, s[at % NV], lane0 + at / NV * SH);
+                    const float2 p = make_float2(w, w);
+#pragma unroll
+                    for (int x = 0; x < EL / 4; ++x) {
+                        o[r][2 * x] = tc::fma2(p, make_float2(v[x].x, v[x].y), o[r][2 * x]);
+                        o[r][2 * x + 1] = tc::fma2(p, make_float2(v[x].z, v[x].w), o[r][2 * x + 1]);
                     }
                 }
             }
@@ -741,6 +767,16 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
         cp_wait<0>();
         __syncwarp();  // the ring is filled anew
         // join the NG token groups of the warp
+#pragma unroll
+        for (int x = 0; x < NV; ++x)
+#pragma unroll
+            for (int y = RT * SH / NV; y < LT; y <<= 1) l_own[x] += __shfl_xor_sync(0xffffffffu, l_own[x], y);
+        float m[RT], l[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            m[r] = __shfl_sync(0xffffffffu, m_own[r % NV], lane - e + r / NV * SH);
+            l[r] = __shfl_sync(0xffffffffu, l_own[r % NV], lane - e + r / NV * SH);
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             float M = m[r];
@@ -848,7 +884,7 @@ PagedShape paged_decode_shape(int dtype, int rows, int d)
         s.kind = kPagedF32;
         s.WR = s.R = rows <= 4 ? 4 : 8;
         s.unit = 1024 / s.DP;
-        s.min_units = 8;  // 8 sequences of up to 4K: 6 units 29.2 us, 8 27.0
+        s.min_units = 3;  // 15 sequences of up to 700 tokens: 8 units 33 us, 4 27, 3 23
         s.item_units = 4;
         s.workers = 8 * kNumSMs;
     }
