@@ -176,6 +176,50 @@ CSA_DEV int paged_places(const PagedAttnArgs& a, int base, int NB, PagedScratch<
     return tid < n ? sc.places[tid] : 0;
 }
 
+CSA_DEV PagedEntry shfl_entry(const PagedEntry& e, int lane)
+{
+    PagedEntry r;
+    auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, lane); };
+    r.b = get(e.b); r.tile = get(e.tile);
+    r.s1 = get(e.s1); r.w0 = get(e.w0); r.n = get(e.n);
+    r.lo_max = get(e.lo_max); r.hi_min = get(e.hi_min);
+    r.lo_min = get(e.lo_min); r.hi_max = get(e.hi_max); r.sink = get(e.sink);
+    return r;
+}
+
+// The run's first item from its place in the list; `start`: places of a key head before entry c.e.
+CSA_DEV void paged_locate(const PagedAttnArgs& a, PagedCursor& c, int64_t start, int H)
+{
+    const int64_t off = c.at - start * H;
+    const int places = c.en.n + a.item_units;
+    c.h = (int)(off / places);
+    c.u = (int)(off - (int64_t)c.h * places);
+}
+
+// paged_schedule with a run for each warp, 32 entries at most: each warp has them in its lanes and waits for no
+// other (17 sequences of up to 289 tokens, width 256: 17.4 -> 16.3 us).
+CSA_DEV bool paged_schedule_few(const PagedAttnArgs& a, int run, PagedCursor& c)
+{
+    const int lane = threadIdx.x & 31, NB = a.B * a.n_tiles;
+    const PagedEntry en = paged_entry<1>(a, min(lane, NB - 1));
+    const int n = lane < NB ? en.n + a.item_units : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    c.W = __shfl_sync(0xffffffffu, inc, 31);
+    c.runs = (int)max((int64_t)1, min((int64_t)a.runs, c.W / a.min_units));
+    if (run >= c.runs) return false;
+    c.at = run * c.W / c.runs;
+    c.end = (run + 1) * c.W / c.runs;
+    c.e = __ffs(__ballot_sync(0xffffffffu, c.at < inc)) - 1;
+    c.en = shfl_entry(en, c.e);
+    paged_locate(a, c, __shfl_sync(0xffffffffu, inc - n, c.e), 1);
+    return true;
+}
+
 // T threads call it together, each with the run of its warp (PER_WARP) or of the CTA.  False: that run is empty.
 template <int T, int LANES, bool PER_WARP>
 CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int run, PagedScratch<T, LANES>& sc, PagedCursor& c)
@@ -183,6 +227,7 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int run, PagedScratch<T, LAN
     int64_t* sh = sc.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int NB = a.B * a.n_tiles, H = PER_WARP ? 1 : a.n_kv;  // heads in a list
+    if (PER_WARP && NB <= 32) return paged_schedule_few(a, run, c);
     int64_t sum = 0;
     int n0 = 0;
     for (int base = 0; base < NB; base += T) {
@@ -231,11 +276,8 @@ CSA_DEV bool paged_schedule(const PagedAttnArgs& a, int run, PagedScratch<T, LAN
     }
     __syncthreads();  // sc may be reused
     if (!some) return false;
-    const int64_t off = c.at - start * H;
     c.en = paged_entry<(LANES > 1 ? 32 : 1)>(a, c.e);
-    const int places = c.en.n + a.item_units;
-    c.h = (int)(off / places);
-    c.u = (int)(off - (int64_t)c.h * places);
+    paged_locate(a, c, start, H);
     return true;
 }
 

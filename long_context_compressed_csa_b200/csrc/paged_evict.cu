@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
         if (C == 1) __syncthreads();  // found and hist are written again
     }
     // keys above `prefix` stay, and the first `want` of those equal to it
-    auto rows_of = [&](int64_t c0, auto use) {  // use(token, tokens that stay, tokens equal) for each row of the warp
+    auto rows_of = [&](int64_t c0, auto use) {  // use(token, key, tokens that stay, tokens equal) for each row of the warp
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
             if (i >= rows) break;
@@ -214,13 +214,13 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
             const bool safe = j < first || j >= last;
             const unsigned up = __ballot_sync(0xffffffffu, x < len && (safe || (!none && key[i] > prefix)));
             const unsigned eq = __ballot_sync(0xffffffffu, x < len && !safe && !none && key[i] == prefix);
-            use((int)j, up, eq);
+            use((int)j, key[i], up, eq);
         }
     };
     int n_above = 0, n_tie = 0;
     for (int64_t c0 = 0; c0 < len; c0 += chunk) {
         if (reload) load(c0);
-        rows_of(c0, [&](int, unsigned up, unsigned eq) {
+        rows_of(c0, [&](int, uint32_t, unsigned up, unsigned eq) {
             n_above += __popc(up);
             n_tie += __popc(eq);
         });
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
         if (reload) {
             load(c0);
             n_above = n_tie = 0;
-            rows_of(c0, [&](int, unsigned up, unsigned eq) {
+            rows_of(c0, [&](int, uint32_t, unsigned up, unsigned eq) {
                 n_above += __popc(up);
                 n_tie += __popc(eq);
             });
@@ -258,13 +258,14 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
         int w_tie = ties + block_scan<T>(own_tie, sh, all_tie) - own_tie;
         w_above = __shfl_sync(0xffffffffu, w_above, 0);
         w_tie = __shfl_sync(0xffffffffu, w_tie, 0);
-        rows_of(c0, [&](int j, unsigned up, unsigned eq) {
+        rows_of(c0, [&](int j, uint32_t k, unsigned up, unsigned eq) {
             const unsigned below = (1u << lane) - 1;
             const int at_tie = w_tie + __popc(eq & below);
             if ((up >> lane & 1) || ((eq >> lane & 1) && at_tie < want)) {
                 const int at = w_above + __popc(up & below) + min(at_tie, want);  // those before it that stay
                 idx[at] = j;
-                new_acc[at] = acc[j];
+                // the key is the weight, but for a NaN and a zero of either sign
+                new_acc[at] = k == 0 || k == 0x80000000u ? acc[j] : key_to_float(k);
             }
             w_above += __popc(up);
             w_tie += __popc(eq);
