@@ -43,7 +43,7 @@ struct PagedAttnArgs {
     // cut into tiles of R rows; an entry e = b * n_tiles + tile and a key head make one item.
     int R, n_tiles;
     int unit;              // cached tokens of a schedule unit
-    int min_units;         // units a CTA takes at least
+    int min_units;         // places a run has at least
     int item_units;        // what an item costs beside its units, in units
     int runs;              // runs of the schedule
     int heads;             // lists of runs: worker w has run w / heads (prompt and CUDA-core kernels: one list, a worker
@@ -68,7 +68,7 @@ struct RowBounds { int lo, hi, sink; };
 CSA_DEV RowBounds paged_bounds_at(const PagedAttnArgs& a, int64_t t)
 {
     RowBounds r;
-    r.hi = t < 0 ? 0 : (int)min(t + 1, (int64_t)a.cap);
+    r.hi = t < 0 ? 0 : t >= a.cap ? a.cap : (int)t + 1;
     r.lo = a.n_win > 0 ? (int)min(max(t - a.n_win + 1, (int64_t)0), (int64_t)r.hi) : 0;
     r.sink = min(a.n_sink, r.lo);
     return r;

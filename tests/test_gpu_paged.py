@@ -708,3 +708,17 @@ def test_counts_that_do_not_fit_are_refused():
             lib.paged_attn(q, K, V, table, t, out, ws, **kw)
     with pytest.raises(lib.CSAError):
         lib.paged_attn(q, K, V, table, t, out, ws, n_win=-1)
+
+
+@pytest.mark.parametrize("nq", [2, 40])
+def test_attn_positions_at_the_ends_of_64_bits(nq):
+    K, V = pools(6, 16, 2, 64, torch.bfloat16, 5)
+    table = torch.tensor([[0, 1], [2, 3], [4, 5]], dtype=torch.int32, device=DEV)
+    q = randn((3, nq, 4, 64), 9).to(DEV)
+    t = torch.full((3, nq), 2**63 - 1, dtype=torch.int64)
+    t[1, 0], t[2] = 5, -2**63
+    t = t.to(DEV)
+    P = weight_bits(nq, 4, 2, 64, torch.bfloat16, False)
+    for n_win, n_sink in ((0, 0), (4, 2)):
+        out, lse, _ = run_attn(q, K, V, table, t, n_win, n_sink)
+        check_attn(q, K, V, table, t, out, lse, P, n_win, n_sink)
