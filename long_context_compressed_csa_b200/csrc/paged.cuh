@@ -103,16 +103,19 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
     const int i0 = row0 / a.G, i1 = row1 / a.G;
     const int64_t* ts = a.t + (int64_t)r.b * a.nq;
     constexpr int kAhead = LANES > 1 ? 8 : 1;  // loads under way at once
-    int64_t t_min = INT64_MAX, t_max = INT64_MIN, t_seen = INT64_MAX;  // t_seen: the smallest t >= 0
+    // t + 1 in 32 bits, 0 for padding: past the last window that reaches the cache one t is as good as another
+    const int64_t far = (int64_t)a.cap + a.n_win;
+    uint32_t t_min = UINT32_MAX, t_max = 0, t_seen = UINT32_MAX;  // t_seen: the smallest t >= 0
     for (int i = i0 + (LANES > 1 ? (int)(threadIdx.x & (LANES - 1)) : 0); i <= i1; i += LANES * kAhead) {
         int64_t t[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) t[k] = ts[min(i + k * LANES, i1)];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            t_min = min(t_min, t[k]);
-            t_max = max(t_max, t[k]);
-            if (t[k] >= 0) t_seen = min(t_seen, t[k]);
+            const uint32_t x = t[k] < 0 ? 0u : (uint32_t)min(t[k], far) + 1;
+            t_min = min(t_min, x);
+            t_max = max(t_max, x);
+            t_seen = min(t_seen, x - 1);  // padding: the largest
         }
     }
 #pragma unroll
@@ -121,10 +124,10 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
         t_max = max(t_max, __shfl_xor_sync(0xffffffffu, t_max, o));
         t_seen = min(t_seen, __shfl_xor_sync(0xffffffffu, t_seen, o));
     }
-    const RowBounds first = paged_bounds_at(a, t_min), last = paged_bounds_at(a, t_max);
+    const RowBounds first = paged_bounds_at(a, (int64_t)t_min - 1), last = paged_bounds_at(a, (int64_t)t_max - 1);
     r.lo_max = last.lo;
     r.hi_min = first.hi;
-    r.lo_min = t_max >= 0 ? paged_bounds_at(a, t_seen).lo : INT32_MAX;
+    r.lo_min = t_max > 0 ? paged_bounds_at(a, t_seen).lo : INT32_MAX;
     r.hi_max = last.hi;
     r.sink = last.sink;
     r.w0 = r.hi_max > 0 ? r.lo_min / a.unit : 0;
