@@ -393,7 +393,7 @@ int hca_dense_attn_window(const void* q, const void* cache, const int64_t* t, co
  * anything, NaN included: they reach no result.  A NaN or an infinity in a row that some query sees may reach all
  * queries of the same sequence and key head in that call.
  * Layouts: any alignment of whole elements is right; rows that start on 16 bytes and are whole 16-byte words are
- * what the fast kernels take, and a prompt (17 packed rows nq * G or more, bf16, d <= 128) also wants pages
+ * what the fast kernels take, and a prompt (33 packed rows nq * G or more, bf16, d <= 128) also wants pages
  * of a multiple of 8 rows.
  * ------------------------------------------------------------------------------- */
 

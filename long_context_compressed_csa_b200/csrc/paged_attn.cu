@@ -335,8 +335,10 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
 
 // The kernel of a call, by its rows (queries x heads of a key head), type and layout.  `wide`: every
 // row can be loaded 16 bytes at a time; what cannot takes the CUDA-core kernel.  `boxes`: the pools can be
-// read by TMA.  A tile of 128 rows costs the prompt kernel the same however few of them there are.
-constexpr int kPromptRows = 17;
+// read by TMA.  A tile of 128 rows costs the prompt kernel the same however few of them there are: 16 sequences of 8K
+// tokens, d = 128, prompt kernel against decode kernel: 24 rows of 8 key heads 149 and 116 us, 32 of 2 key heads 54 and
+// 49, 64 55 and 71, 128 57 and 121.
+constexpr int kPromptRows = 33;
 static PagedShape paged_shape(int dtype, bool wide, bool boxes, int rows, int d)
 {
     if (wide && boxes && dtype == CSA_BF16 && rows >= kPromptRows && d <= 128) return paged_prompt_shape(d);
