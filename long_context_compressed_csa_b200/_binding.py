@@ -366,16 +366,24 @@ def hca_dense_attn(q, cache, t, m_prime, out, workspace, lse=None, scale=0.0, st
 
 
 # The paged calls take a few microseconds on the GPU in a decode step, so their checks are written for time:
-# one comparison for each thing that may differ.
-def _here(stream, *ts):
+# one comparison for each thing that may differ, torch looked up once.
+torch = None
+
+
+def _here(stream, first, *ts):
     """The paged calls launch on the current device; tensors of another one are refused.  Returns the raw stream."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    global torch
+    if torch is None:
+        import torch as _torch
+        torch = _torch
+    dev = first.get_device()
     for t in ts:
         if t is not None and t.get_device() != dev:
-            if not t.is_cuda:
-                raise ValueError("all tensors must be CUDA tensors")
-            raise ValueError("all tensors must be on the current device (cuda:%d)" % torch.cuda.current_device())
+            dev = -1
+    if dev < 0:
+        _cuda(first, *ts)
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("all tensors must be on the current device (cuda:%d)" % torch.cuda.current_device())
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -395,7 +403,6 @@ def _i32(*xs):
 def _pool(K, V, table, B):
     """Strides and sizes of the pools K, V [n_pages, page, n_kv, d] (any page, row and head
     strides, so a permuted [n_pages, n_kv, page, d] pool too) and of the page table [B, max_pages]."""
-    import torch
     shape, strides = K.shape, K.stride()
     n_pages, page, n_kv, d = shape
     assert V.shape == shape and V.stride() == strides and V.dtype == K.dtype
@@ -409,7 +416,6 @@ def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
     """Write the keys and values k, v [B,nq,n_kv,d] (any strides, last dim contiguous) of new tokens
     into the pools [n_pages,page,n_kv,d] at cache positions t int64 [B,nq] (< 0: padding), through
     the page table int32 [B,max_pages]."""
-    import torch
     raw = _here(stream, k, v, K_pages, V_pages, table, t)
     shape, strides = k.shape, k.stride()
     B, nq = shape[:2]
@@ -434,7 +440,6 @@ def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.
 
     acc fp32 [B,n_kv,cap]: acc_out (acc itself if None) = acc + the weight that each cached token
     got, summed over the queries and the query heads of its key head."""
-    import torch
     raw = _here(stream, q, K_pages, V_pages, table, t, out, workspace, lse, acc, acc_out)
     shape = q.shape
     B, nq, n_h, d = shape
@@ -461,7 +466,6 @@ def paged_evict(K_pages, V_pages, table, lens, acc, keep, new_table, new_lens, n
     last n_recent and the heaviest of the others by acc fp32 [B,n_kv,cap], moved in their order to
     the pages of new_table int32 [B,new_max_pages] (none of them in table).  Writes new_lens int64
     [B], new_acc fp32 [B,n_kv,new_cap] and the old positions idx_out int32 [B,n_kv,keep] (-1 = none)."""
-    import torch
     raw = _here(stream, K_pages, V_pages, table, lens, acc, new_table, new_lens, new_acc, idx_out)
     B = table.shape[0]
     pool, n_kv, d, cap = _pool(K_pages, V_pages, table, B)

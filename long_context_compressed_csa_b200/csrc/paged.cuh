@@ -1,6 +1,8 @@
 // The paged key-value cache of the full-attention layers: arguments, visibility, and the
 // device-side schedule that the attention kernels share.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace csa {
@@ -404,6 +406,22 @@ inline int paged_runs(const PagedShape& s, int64_t lists, int64_t places)
 }
 PagedShape paged_decode_shape(int dtype, int rows, int d);
 int launch_paged_decode(const PagedAttnArgs& a, const PagedShape& s, cudaStream_t stream);
+
+// Lets a kernel have `smem` bytes of dynamic shared memory, once on each device (the call costs as much as a tenth of
+// a decode step's host time).
+template <auto kKernel>
+inline bool paged_allow_smem(int smem)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return true;
+}
 
 bool paged_prompt_takes(const PagedPool& pl, int n_kv, int d);
 PagedShape paged_prompt_shape(int d);

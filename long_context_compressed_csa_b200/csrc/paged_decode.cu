@@ -820,19 +820,15 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
     }
 }
 
-template <typename F>
-int launch(F* kern, int threads, int groups, int smem, PagedAttnArgs a, cudaStream_t stream)
+template <auto kKernel>
+int launch(int threads, int groups, int smem, PagedAttnArgs a, cudaStream_t stream)
 {
     // few workers: one or two on every SM, not eight on a few
     const int workers = a.runs * a.heads;
     a.per_cta = (workers + kNumSMs - 1) / kNumSMs;
     if (a.per_cta > groups) a.per_cta = groups;
-    // per device and idempotent; no state is kept between calls
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return CSA_ERR_CUDA;
-    }
-    launch_pdl(kern, dim3((workers + a.per_cta - 1) / a.per_cta), dim3(threads), smem, stream, a);
+    if (!paged_allow_smem<kKernel>(smem)) return CSA_ERR_CUDA;
+    launch_pdl(kKernel, dim3((workers + a.per_cta - 1) / a.per_cta), dim3(threads), smem, stream, a);
     return launch_status();
 }
 
@@ -840,19 +836,19 @@ template <int DP, int WR>
 int launch_mma(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = MmaShape<DP, WR>;
-    return launch(paged_attn_mma<DP, WR>, S::kThreads, S::kGroups, S::kSmem, a, stream);
+    return launch<paged_attn_mma<DP, WR>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
 template <int DP>
 int launch_few(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = FewShape<DP>;
-    return launch(paged_attn_few<DP>, S::kThreads, S::kGroups, S::kSmem, a, stream);
+    return launch<paged_attn_few<DP>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
 template <int DP, int RT>
 int launch_f32(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = F32Shape<DP, RT>;
-    return launch(paged_attn_f32<DP, RT>, S::kThreads, S::kWarps, S::kSmem, a, stream);
+    return launch<paged_attn_f32<DP, RT>>(S::kThreads, S::kWarps, S::kSmem, a, stream);
 }
 
 }  // namespace

@@ -612,10 +612,7 @@ template <int DP>
 int launch(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box_rows, cudaStream_t stream)
 {
     constexpr int smem = PromptShape<DP>::kSmem;
-    if (cudaFuncSetAttribute(paged_attn_prompt<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return CSA_ERR_CUDA;
-    }
+    if (!paged_allow_smem<paged_attn_prompt<DP>>(smem)) return CSA_ERR_CUDA;
     launch_pdl(paged_attn_prompt<DP>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
     return launch_status();
 }
