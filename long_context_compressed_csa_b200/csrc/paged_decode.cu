@@ -389,7 +389,9 @@ struct FewShape {
 //   S^T (16 tokens x 8 rows) = K Q^T,   O^T (16 columns x 8 rows) += V^T P^T.
 // A lane has two rows (2 (lane mod 4) and the next) and tokens, or columns, lane / 4 and 8 more.  P^T becomes the
 // second product's operand by a transposition of its 8 x 8 blocks.  Half the tensor work and half the logits a
-// lane of the 16-row kernel, whose time and power (not the cache's bytes alone) bounded long decodes.
+// lane of the 16-row kernel, whose time and power (not the cache's bytes alone) bounded long decodes: two
+// sequences of 256K tokens, width 64: 185 -> 168 us, 6.4 TB/s; 16 of up to 128K, 8 rows: 320 us, 6.6 TB/s, and at the
+// power cap 330 where the 16-row kernel took 372.
 template <int DP>
 __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(PagedAttnArgs a)
 {
@@ -581,6 +583,9 @@ __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(Page
     }
 }
 
+// fp32 rows: RT of them in registers, EL = 64 / RT elements of a row a lane, so that q and the output take 128
+// registers for either RT.  Bound by FMA and shuffle issue at 8 rows (16 sequences of up to 8K tokens, 545 MB: 126 us,
+// 4.3 TB/s), by latency in small calls (8 of up to 4K, 69 MB: 26 us).
 template <int DP, int RT>
 struct F32Shape {
     static constexpr int kEL = 64 / RT;      // elements of a row that a lane has

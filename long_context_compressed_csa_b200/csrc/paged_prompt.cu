@@ -21,6 +21,9 @@
 // The masks (positions, window, first tokens, missing pages) are applied to S only in units that
 // are not wholly visible; there the rows of V that no query sees are set to zero too, since 0 x NaN
 // would reach the sums.  Bounded waits: a timeout ends the CTA and sets its status.
+// 2 x 1024 queries over 15-16K tokens, 64 / 8 heads, d = 128: 923 us, 1104 TFLOP/s, 0.68 of the measured GEMM (1050 to
+// 1109 us at the power cap).  A unit of both tiles takes 3500 clocks, 2048 of which are products: a tile's
+// softmax (2100) and its products (1100 with their barriers) take turns, and there is no TMEM for a second S.
 #include "paged.cuh"
 #include "tc_utils.cuh"
 
