@@ -7,15 +7,19 @@
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread per row: S from TMEM to registers,
 //                   running maximum and sum, P (bf16) over S in TMEM; q -> shared memory before, O ->
 //                   memory after a segment
-//   warp 8          TMA loads of K and V, one box of up to 128 rows of one page per lane; a page that is
+//   warps 8, 10     TMA loads of K and of V, one box of up to 128 rows of one page per lane; a page that is
 //                   not there, or that no row sees, is a box outside the tensor: zeros
 //   warp 9          MMA issue
-// One tile's softmax runs while the other's products do.  P replaces S in TMEM, half by half, so
+// One tile's softmax runs while the other's products do.  Where every item is one tile (kOne) both warpgroups work on it:
+// they take its units in turn, each with its own S, O, maximum and sum, and warps 0-3 join the two at the end: 40 rows
+// of 8 key heads, 16 sequences of 8K tokens in pages of 64, d = 128 and 64: 122 -> 100 us and 98 -> 71 (64 of 400: 63 ->
+// 57 and 47 -> 43).  A kernel of its own: in one kernel with the two-tile form the added registers cost prompts 4 to 9%.
+// P replaces S in TMEM, half by half, so
 // the first half's product with V starts under the second's exponentials, and S(j+1) follows P(j) V.
 // (Two S of 64 tokens a tile, so that S(j+1) is there before P(j), measured slower: a product of
 // N = 64 takes as long as one of 128, since the operand q is read from shared memory either way.)
 // O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8).  S(j) is
-// issued after P(j-1) V, so once S(j) is there O is at rest, and the softmax thread rescales its
+// issued after the P V before it of its O, so once S(j) is there O is at rest, and the softmax thread rescales its
 // row in TMEM by itself.  P is rounded to bf16 (half a step is 2^-9 to 2^-8 of a weight), as the
 // operand of the tensor core has to be; the row sum takes the weights before the rounding.
 // The masks (positions, window, first tokens, missing pages) are applied to S only in units that
@@ -33,8 +37,8 @@ namespace {
 constexpr int kM = 128;             // rows of a tile
 constexpr int kT = 128;             // cached tokens of a unit
 constexpr int kH = 64;              // of a half: P is handed over in two
-constexpr int kThreads = 384;       // two softmax warpgroups, and one of which two warps work
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;       // two softmax warpgroups, and one of which three warps work
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
 // Registers of a thread: launched with 168, then split between the warpgroups (a row of S is 128 of them).
 constexpr int kRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kRegs, "no more than the CTA was launched with");
@@ -108,7 +112,7 @@ CSA_DEV uint32_t pages32(uint32_t have, int x)
     return (h & 1) * 0xffu | (h >> 1 & 1) * 0xff00u | (h >> 2 & 1) * 0xff0000u | (h >> 3 & 1) * 0xff000000u;
 }
 
-template <int DP>
+template <int DP, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ PagedAttnArgs a, const int box_rows)
@@ -121,9 +125,9 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     uint8_t* sK = smem + 2 * S::kTile;     // [NS]
     uint8_t* sV = sK + NS * S::kTile;      // [NS]
     uint8_t* sO = sV + NS * S::kTile;      // [8 warps][32 rows][128 bytes]
-    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS], drained;
-    // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S; by the time
-    // of unit n the V stage of n - NS - 1 has been free, so n - 2 NS is long past.
+    __shared__ uint64_t Qfull[2], Sfull[2], Pready[2][2], Ofull[2], Joined, Kfull[NS], Kempty[NS], Vfull[NS], Vempty[NS], drained;
+    // Of a unit: bit i: rows 8 i .. 8 i + 7 have a page.  Written before its K, read after its S, before its P; K of
+    // unit n is written once S(n - NS) is done, which follows P(n - NS - 2), so unit n - 2 NS has been read.
     __shared__ uint32_t have[2 * NS];
     __shared__ uint32_t tmem_slot;
     // before the first tiles arrive
@@ -138,6 +142,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             for (int half = 0; half < 2; ++half) tc::mbar_init(&Pready[i][half], kM / 32);
             tc::mbar_init(&Ofull[i], 1);
         }
+        tc::mbar_init(&Joined, kM / 32);
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&Kfull[i], 1);
             tc::mbar_init(&Kempty[i], 1);
@@ -186,10 +191,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         const int w = warp >> 2, r = tid & (kM - 1);  // tile, row in it
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tS(w) + quarter, o_at = tO(w) + quarter;
-        uint32_t n_s = 0, n_o = 0, n_v = 0;  // units and segments of this tile, V tiles: the barriers' phases
+        constexpr int kStep = kOne ? 2 : 1;                     // of a warpgroup's units
+        const int row0 = kOne ? 0 : w * kM, unit0 = kOne ? w : 0;  // its first row and unit
+        const bool has_q = !kOne || w == 0;
+        // units and segments (and joins) of this warpgroup, V tiles: the barriers' phases
+        uint32_t n_s = 0, n_o = 0, n_v = 0;
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
-            bool tile, in;  // the tile has rows; this is one
+            bool tile, in;  // the warpgroup's tile has rows; this is one
             int64_t at;
             RowBounds rb;
         };
@@ -201,10 +210,10 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         auto row_of = [&](const PagedEntry& en, int h) {
             Row x;
             const int n_rows = paged_rows(a, en.tile);
-            x.tile = w * kM < n_rows;
-            x.in = w * kM + r < n_rows;
-            x.at = x.in ? paged_out_row(a, en.b, en.tile, h, w * kM + r) : 0;
-            x.rb = x.in ? paged_bounds(a, en.b, (en.tile * a.R + w * kM + r) / a.G) : RowBounds{0, 0, 0};
+            x.tile = kOne || row0 < n_rows;
+            x.in = row0 + r < n_rows;
+            x.at = x.in ? paged_out_row(a, en.b, en.tile, h, row0 + r) : 0;
+            x.rb = x.in ? paged_bounds(a, en.b, (en.tile * a.R + row0 + r) / a.G) : RowBounds{0, 0, 0};
             return x;
         };
         // q of the warp's 32 rows, kC lanes to a row
@@ -262,7 +271,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         Row row;
         if (more) {
             row = row_of(cur.en, cur.h);
-            if (row.tile) {
+            if (has_q && row.tile) {
                 load_q(row);
                 give_q();
             }
@@ -273,9 +282,9 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             float m = -INFINITY, l = 0.f;  // m: what the weights in O and l are relative to
             if (row.tile) {
                 float* lg = a.logits && row.in ? a.logits + (((int64_t)b * a.n_kv + h) * (a.nq * a.G) +
-                                                             tile * a.R + w * kM + r) * a.cap
+                                                             tile * a.R + row0 + r) * a.cap
                                                : nullptr;
-                for (int u = sg.u0; u < sg.u1; ++u, ++n_s) {
+                for (int u = sg.u0 + unit0; u < sg.u1; u += kStep, ++n_s) {
                     const uint32_t vt = n_v + (uint32_t)(u - sg.u0), vs = vt % NS;
                     ok = all(wait(&Sfull[w], n_s));
                     if (!ok) break;
@@ -333,7 +342,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         const float f = grow ? exp2f(m - top) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (u > sg.u0) {  // before the first product O holds nothing of this segment
+                        if (u > sg.u0 + unit0) {  // before the first product O holds nothing of this segment
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 32) {
                                 uint32_t o[16], o1[16];
@@ -392,17 +401,39 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
             if (more) {
                 row = row_of(cur.en, cur.h);
-                // S of the last unit was there: no product reads q any more
-                if (row.tile) load_q(row);
+                // S of the last unit was there: no product reads q any more, but the other warpgroup's of the same tile
+                if (!kOne && row.tile) load_q(row);
             }
             if (out.tile && ok) ok = all(wait(&Ofull[w], n_o++));
             if (!ok) break;
             // every product of the segment is done
-            if (more && row.tile) give_q();
-            if (out.tile) {
+            if (more && has_q && row.tile) {
+                if (kOne) load_q(row);
+                give_q();
+            }
+            // Warps 4-7 leave their maximum and sum in their part of sO.  Warps 0-3 have read it, and O of both, before
+            // they hand over the first P of the next segment, which its products and Ofull follow.
+            if (kOne && w == 1) {
+                reinterpret_cast<float2*>(sO + warp * (32 * 128))[lane] = make_float2(m, l);
+                arrive(&Joined);
+            } else if (out.tile) {
+                float fa = 1.f, fb = 0.f;
+                if constexpr (kOne) {
+                    ok = all(wait(&Joined, n_o - 1));
+                    if (!ok) break;
+                    const float2 ml = reinterpret_cast<const float2*>(sO + (warp + 4) * (32 * 128))[lane];
+                    const float top = fmaxf(m, ml.x);
+                    fa = m == -INFINITY ? 0.f : exp2f(m - top);
+                    fb = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+                    m = top;
+                    l = l * fa + ml.y * fb;
+                }
+                const bool two = kOne && done.u1 - done.u0 > 1;  // else nothing was written to the other O
                 tc::fence_after_sync();
-                const int64_t slot = (int64_t)done.slot * a.R + w * kM + r;
+                const int64_t slot = (int64_t)done.slot * a.R + row0 + r;
                 const float inv = done.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                fa *= inv;
+                fb *= inv;
                 // through shared memory, so that a warp writes whole lines: 128 bytes of each of its rows at a time,
                 // 16-byte chunks swizzled by the row
                 uint8_t* so = sO + warp * (32 * 128);
@@ -432,7 +463,15 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     tc::tmem_ld32_async(o_at + x, o);
                     tc::tmem_wait_ld_regs(o);
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+                    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fa);
+                    if (two) {
+                        uint32_t o1[32];
+                        tc::tmem_ld32_async(tO(1) + quarter + x, o1);
+                        tc::tmem_wait_ld_regs(o1);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            o[y] = __float_as_uint(fmaf(__uint_as_float(o1[y]), fb, __uint_as_float(o[y])));
+                    }
                     if (bf16) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -451,7 +490,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 }
                 if (out.in) {
                     if (done.whole)
-                        paged_store_lse(a, out.at, b, tile, h, w * kM + r, m, l);
+                        paged_store_lse(a, out.at, b, tile, h, row0 + r, m, l);
                     else
                         a.part_ml[slot] = make_float2(m, l);
                 }
@@ -461,8 +500,14 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
     } else if (some) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kLoadWarp) {
-            // ------------------------------------------------------------ K and V
+        if (warp == kKWarp || warp == kVWarp) {
+            // ------------------------------------------------------------ K or V
+            // a warp each: K of the units ahead does not wait for a free stage of V, and twice as many small boxes are
+            // asked for (one tile by one warpgroup, pages of 16, d = 128: 141 -> 124 us; pages of 64: the same within 3%)
+            const bool is_v = warp == kVWarp;
+            const CUtensorMap* const map = is_v ? &map_v : &map_k;
+            uint64_t *const fulls = is_v ? Vfull : Kfull, *const empties = is_v ? Vempty : Kempty;
+            uint8_t* const tiles = is_v ? sV : sK;
             tc::fence_proxy_async_smem();  // the schedule's scratch, before the tiles over it
             uint32_t n = 0;  // tiles begun
             bool ok = true;
@@ -485,34 +530,26 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                     const unsigned there = __ballot_sync(0xffffffffu, page != none);
                     uint32_t hv = 0;
                     for (int i = 0; i < kT / 8; ++i) hv |= (there >> (i * 8 / box_rows) & 1u) << i;
-                    const uint32_t st = n % NS, ph = n / NS + 1;  // waits of the first round pass at once
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        uint64_t *full = kv ? &Vfull[st] : &Kfull[st], *empty = kv ? &Vempty[st] : &Kempty[st];
-                        ok = all(wait(empty, ph));
-                        if (!ok) break;
-                        if (lane == 0) {
-                            if (!kv) have[n % (2 * NS)] = hv;
-                            tc::mbar_arrive_expect_tx(full, S::kTile);
-                        }
-                        __syncwarp();
-                        if (lane < boxes) {
-                            uint8_t* dst = (kv ? sV : sK) + st * S::kTile + lane * box_rows * 128;
-#pragma unroll
-                            for (int x = 0; x < S::kPanels; ++x)
-                                tma_load_4d(dst + x * (kT * 128), kv ? &map_v : &map_k, full, x * 64, c.h, in, page);
-                        }
-                    }
+                    const uint32_t st = n % NS;
+                    ok = all(wait(&empties[st], n / NS + 1));  // of the first round: passes at once
                     if (!ok) break;
+                    if (lane == 0) {
+                        if (!is_v) have[n % (2 * NS)] = hv;
+                        tc::mbar_arrive_expect_tx(&fulls[st], S::kTile);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        uint8_t* dst = tiles + st * S::kTile + lane * box_rows * 128;
+#pragma unroll
+                        for (int x = 0; x < S::kPanels; ++x)
+                            tma_load_4d(dst + x * (kT * 128), map, &fulls[st], x * 64, c.h, in, page);
+                    }
                 }
                 if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
             // no copy is in flight when the CTA ends: on the normal path the products have waited for them
             if (!ok)
-                for (uint32_t k = n >= NS ? n - NS + 1 : 0; k <= n; ++k) {
-                    wait(&Kfull[k % NS], k / NS);
-                    wait(&Vfull[k % NS], k / NS);
-                }
+                for (uint32_t k = n >= NS ? n - NS : 0; k < n; ++k) wait(&fulls[k % NS], k / NS);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ products
             constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
@@ -527,11 +564,11 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             const uint32_t q0 = (uint32_t)dk + (tc::smem_u32(sQ) >> 4), k0 = (uint32_t)dk + (tc::smem_u32(sK) >> 4),
                            v0 = (uint32_t)dv + (tc::smem_u32(sV) >> 4);
             const uint32_t dk_hi = (uint32_t)(dk >> 32), dv_hi = (uint32_t)(dv >> 32);
-            constexpr uint32_t kStep = S::kTile >> 4;
+            constexpr uint32_t kTileStep = S::kTile >> 4;
             auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
             // by the elected lane
             auto mma_s = [&](int w, uint32_t st) {
-                const uint32_t q = q0 + w * kStep, k = k0 + st * kStep;
+                const uint32_t q = q0 + (kOne ? 0 : w * kTileStep), k = k0 + st * kTileStep;
 #pragma unroll
                 for (int x = 0; x < DP / 16; ++x) {
                     const uint32_t at = ((x >> 2) * (kM * 128) + (x & 3) * 32) >> 4;
@@ -540,7 +577,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 tc::mma_commit(&Sfull[w]);
             };
             auto mma_o = [&](int w, uint32_t st, int half, bool more) {
-                const uint32_t v = v0 + st * kStep;
+                const uint32_t v = v0 + st * kTileStep;
 #pragma unroll
                 for (int x = half * (kH / 16); x < (half + 1) * (kH / 16); ++x)
                     mma_bf16_ts(tO(w), tS(w) + x * 8, desc(v + (x * 16 * 128 >> 4), dv_hi), kIdescO,
@@ -549,7 +586,55 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             while (ok) {
                 const PagedSegment sg = paged_segment(a, c, cta);
                 if (sg.u0 == sg.u1) break;
-                const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1, n_u = sg.u1 - sg.u0;
+                const int n_u = sg.u1 - sg.u0;
+                if constexpr (kOne) {
+                    // The units in turn, S two units ahead.  No wait is for a K or V that needs a later step: K(u + 2)
+                    // takes a stage that S(u) has left at the latest, V(u) one that P(u - 2) V has (NS >= 2).
+                    ok = all(wait(&Qfull[0], n_q[0]++));
+                    for (int w = 0; w < 2 && w < n_u && ok; ++w) {
+                        const uint32_t st = (n + w) % NS;
+                        ok = all(wait(&Kfull[st], (n + w) / NS));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (elect()) {
+                            mma_s(w, st);
+                            tc::mma_commit(&Kempty[st]);
+                        }
+                        __syncwarp();
+                    }
+                    for (int u = 0; u < n_u && ok; ++u, ++n) {
+                        const uint32_t st = n % NS, nx = (n + 2) % NS;
+                        const bool more = u + 2 < n_u;
+                        const int w = u & 1;
+                        const uint32_t ph = w ? n_p[1] : n_p[0];
+                        ok = all(wait(&Vfull[st], n / NS)) && all(wait(&Pready[w][0], ph));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (elect()) mma_o(w, st, 0, u > 1);
+                        __syncwarp();
+                        if (more) ok = all(wait(&Kfull[nx], (n + 2) / NS));
+                        ok = ok && all(wait(&Pready[w][1], ph));
+                        if (!ok) break;
+                        ++(w ? n_p[1] : n_p[0]);
+                        tc::fence_after_sync();
+                        if (elect()) {
+                            mma_o(w, st, 1, true);
+                            if (more) {
+                                mma_s(w, nx);
+                                tc::mma_commit(&Kempty[nx]);
+                            }
+                            tc::mma_commit(&Vempty[st]);
+                            if (u + 1 == n_u) {
+                                tc::mma_commit(&Ofull[0]);
+                                tc::mma_commit(&Ofull[1]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok || !paged_next<32, false>(a, c, sg)) break;
+                    continue;
+                }
+                const int tiles = paged_rows(a, c.en.tile) > kM ? 2 : 1;
                 ok = all(wait(&Kfull[n % NS], n / NS));
                 for (int w = 0; w < tiles && ok; ++w) {
                     ok = all(wait(&Qfull[w], n_q[w]++));
@@ -611,12 +696,12 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
 }
 
-template <int DP>
+template <int DP, bool kOne>
 int launch(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box_rows, cudaStream_t stream)
 {
     constexpr int smem = PromptShape<DP>::kSmem;
-    if (!paged_allow_smem<paged_attn_prompt<DP>>(smem)) return CSA_ERR_CUDA;
-    launch_pdl(paged_attn_prompt<DP>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
+    if (!paged_allow_smem<paged_attn_prompt<DP, kOne>>(smem)) return CSA_ERR_CUDA;
+    launch_pdl(paged_attn_prompt<DP, kOne>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
     return launch_status();
 }
 
@@ -657,7 +742,10 @@ int launch_paged_prompt(const PagedAttnArgs& a, const PagedShape& s, cudaStream_
         if (!make_tmap_bf16_4d(i ? &v : &k, i ? a.V : a.K, a.d, a.n_kv, pl.page, pl.n_pages, ld_head, pl.ld_row, ld_page,
                                64, rows))
             return CSA_ERR_CUDA;
-    return s.DP == 64 ? launch<64>(a, k, v, rows, stream) : launch<128>(a, k, v, rows, stream);
+    // every item has one tile
+    if (a.nq * a.G <= kM)
+        return s.DP == 64 ? launch<64, true>(a, k, v, rows, stream) : launch<128, true>(a, k, v, rows, stream);
+    return s.DP == 64 ? launch<64, false>(a, k, v, rows, stream) : launch<128, false>(a, k, v, rows, stream);
 }
 
 }  // namespace csa

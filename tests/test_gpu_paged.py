@@ -577,6 +577,28 @@ def test_attn_prompts_ragged():
     case([2500], nq=70, n_h=2, n_kv=2, d=128, page=16)
 
 
+@pytest.mark.parametrize("nq,G", [(33, 1), (13, 8), (128, 1), (50, 6)])
+@pytest.mark.parametrize("strong", [0, 1])
+def test_attn_units_of_one_tile_in_turn(nq, G, strong):
+    """Of one row tile the units of 128 tokens are taken in turn by two halves of the kernel: either may hold
+    nearly all of the weight, nothing that a row sees, or no unit at all."""
+    lens = [nq, 129, 256, 257, 1024, 1500, 2900]
+    lens = [max(n, nq) for n in lens]
+    page, d, n_kv = 32, 128, 2
+    B, max_pages = len(lens), -(-max(lens) // page) + 1
+    n_pages = B * max_pages + 2
+    K, V = pools(n_pages, page, n_kv, d, torch.bfloat16, 3)
+    table = tables(B, max_pages, n_pages, 5)
+    for b in range(B):
+        for x in range(max_pages):
+            K[table[b, x].item()] *= 8.0 if x * page // 128 % 2 == strong else 0.125
+    table, t = table.to(DEV), positions(lens, nq).to(DEV)
+    q = randn((B, nq, G * n_kv, d), nq, torch.bfloat16).to(DEV)
+    for n_win, n_sink in ((0, 0), (100, 0), (129, 3)):
+        out, lse, _ = run_attn(q, K, V, table, t, n_win, n_sink)
+        check_attn(q, K, V, table, t, out, lse, weight_bits(nq, G * n_kv, n_kv, d, torch.bfloat16, False), n_win, n_sink)
+
+
 def test_attn_more_key_heads_than_workers():
     case([20, 3], n_h=1300, n_kv=1300, d=8)
     case([20, 3], n_h=1300, n_kv=1300, d=8, dtype=torch.float32)
