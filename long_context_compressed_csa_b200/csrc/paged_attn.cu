@@ -335,9 +335,9 @@ __global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(PagedAttn
 
 // The kernel of a call, by its rows (queries x heads of a key head), type and layout.  `wide`: every
 // row can be loaded 16 bytes at a time; what cannot takes the CUDA-core kernel.  `boxes`: the pools can be
-// read by TMA.  A tile of 128 rows costs the prompt kernel the same however few of them there are: 16 sequences of 8K
-// tokens, d = 128, prompt kernel against decode kernel: 24 rows of 8 key heads 149 and 116 us, 32 of 2 key heads 54 and
-// 49, 64 55 and 71, 128 57 and 121.
+// read by TMA.  A tile of 128 rows costs the prompt kernel the same however few of them there are.  d = 128, pages of 16,
+// prompt kernel against decode kernel: 16 sequences of 8K tokens, 24 rows of 8 key heads 117 and 117 us, 32 of 2 key
+// heads 49 and 50, 64 50 and 71, 128 53 and 121; 24 rows of 64 sequences of 500 67 and 58, of one of 8K 26 and 23.
 constexpr int kPromptRows = 33;
 static PagedShape paged_shape(int dtype, bool wide, bool boxes, int rows, int d)
 {

@@ -14,8 +14,8 @@
 // they take its units in turn, each with its own S, O, maximum and sum, and warps 0-3 join the two at the end: 40 rows
 // of 8 key heads, 16 sequences of 8K tokens in pages of 64, d = 128 and 64: 122 -> 100 us and 98 -> 71 (64 of 400: 63 ->
 // 57 and 47 -> 43).  A kernel of its own: in one kernel with the two-tile form the added registers cost prompts 4 to 9%.
-// P replaces S in TMEM, half by half, so
-// the first half's product with V starts under the second's exponentials, and S(j+1) follows P(j) V.
+// P replaces S in TMEM, half by half, so the first half's product with V starts under the second's exponentials, and
+// the next S of the same place follows P(j) V.
 // (Two S of 64 tokens a tile, so that S(j+1) is there before P(j), measured slower: a product of
 // N = 64 takes as long as one of 128, since the operand q is read from shared memory either way.)
 // O is rescaled only when the running maximum grew by more than 2^8 (P stays below 2^8).  S(j) is
