@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt(PagedAttnArgs a)
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float mn = fmaxf(m[r], top);
                 const float shrink = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
-                const float p = vis ? exp2f(s[r] - mn) : 0.f;
+                // logits of -inf alone leave mn there, and weigh nothing
+                const float p = vis ? exp2f(s[r] - (mn == -INFINITY ? 0.f : mn)) : 0.f;
                 m[r] = mn;
                 l[r] = l[r] * shrink + p;
 #pragma unroll

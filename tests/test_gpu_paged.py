@@ -744,3 +744,33 @@ def test_attn_positions_at_the_ends_of_64_bits(nq):
     for n_win, n_sink in ((0, 0), (4, 2)):
         out, lse, _ = run_attn(q, K, V, table, t, n_win, n_sink)
         check_attn(q, K, V, table, t, out, lse, P, n_win, n_sink)
+
+
+# ==================================================================================
+# values that are not finite: what is seen is told, what is not seen reaches nothing
+# ==================================================================================
+KINDS = [  # a call of each kernel: queries, query heads (two key heads), width, type, layout
+    (1, 8, 64, torch.bfloat16, "nhd"), (1, 8, 256, torch.bfloat16, "nhd"), (2, 16, 128, torch.bfloat16, "nhd"),
+    (3, 16, 128, torch.bfloat16, "nhd"), (12, 8, 256, torch.bfloat16, "nhd"), (10, 8, 128, torch.bfloat16, "hnd"),
+    (90, 8, 64, torch.bfloat16, "nhd"), (1, 4, 64, torch.float32, "nhd"), (2, 8, 128, torch.float32, "hnd"),
+    (1, 4, 256, torch.float32, "nhd"), (2, 6, 64, torch.bfloat16, "odd"), (1, 6, 40, torch.float32, "odd")]
+
+
+@pytest.mark.parametrize("nq,n_h,d,dtype,layout", KINDS)
+def test_attn_logits_of_minus_infinity(nq, n_h, d, dtype, layout):
+    """Weigh nothing: the first tokens, which a kernel meets before any other, and a run of them further on."""
+    lens, page = [40000 if layout == "odd" else 400, 333], 16  # a warp of the CUDA-core kernel has several units
+    max_pages = lens[0] // page + 1
+    K, V = pools(2 * max_pages + 4, page, 2, d, dtype, 11, layout)
+    table = tables(2, max_pages, 2 * max_pages + 4, 4).to(DEV)
+    t = positions(lens, nq).to(DEV)
+    q = randn((2, nq, n_h, d), 9, dtype).abs().clamp(min=2.0 ** -6).to(DEV)
+    hidden = torch.zeros(2, max_pages, dtype=torch.bool, device=DEV)
+    hidden[:, :9], hidden[0, max_pages // 2:max_pages * 3 // 4] = True, True
+    for b in range(2):
+        K[table[b, hidden[b]].long(), :, :, d // 2] = -math.inf
+    out, lse, _ = run_attn(q, K, V, table, t)
+    # the same as if those pages were not there
+    there = torch.where(hidden, -1, table)
+    P = 2.0 ** -16 if layout == "odd" else weight_bits(nq, n_h, 2, d, dtype, False)
+    check_attn(q, torch.nan_to_num(K, neginf=0.0), V, there, t, out, lse, P)
