@@ -351,6 +351,10 @@ CSA_DEV void paged_store_lse(const PagedAttnArgs& a, int64_t o, int b, int tile,
     if (a.lse2) a.lse2[((int64_t)b * a.n_kv + h) * (a.nq * a.G) + tile * a.R + r] = z;
 }
 
+// A piece in which a row saw nothing, or logits of -inf alone.  One of NaN logits has the maximum -inf too (maxima pass a
+// NaN over), but a sum that is NaN, and the joins keep it.
+CSA_DEV bool paged_empty(float m, float l) { return m == -INFINITY && l == 0.f; }
+
 // Rows of tile `tile` that are rows of the call.
 CSA_DEV int paged_rows(const PagedAttnArgs& a, int tile) { return min(a.R, a.nq * a.G - tile * a.R); }
 
@@ -369,10 +373,10 @@ CSA_DEV void paged_finish_segment(const PagedAttnArgs& a, const PagedCursor& c, 
         float L = 0.f, v = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float m = sm_m[w * R + r];
-            if (m == -INFINITY) continue;
+            const float m = sm_m[w * R + r], l = sm_l[w * R + r];
+            if (paged_empty(m, l)) continue;
             const float f = exp2f(m - M);
-            L = fmaf(f, sm_l[w * R + r], L);
+            L = fmaf(f, l, L);
             v = fmaf(f, so[(w * R + r) * ld + col], v);
         }
         if (sg.whole) {

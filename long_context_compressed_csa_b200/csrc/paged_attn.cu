@@ -176,8 +176,8 @@ CSA_DEV void join_pieces(const PagedAttnArgs& a, F slot, int p0, int step, int n
         for (int i = 0; i < NC; ++i) acc[i] *= f;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const float w = p0 + k * step >= np || ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
-            if (w == 0.f) continue;
+            if (p0 + k * step >= np || paged_empty(ml[k].x, ml[k].y)) continue;
+            const float w = exp2f(ml[k].x - M);  // a piece far below the others may still hold a NaN
             L = fmaf(w, ml[k].y, L);
 #pragma unroll
             for (int i = 0; i < NC; ++i) acc[i] = fmaf(w, v[k][i], acc[i]);
@@ -245,14 +245,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_combine(PagedAttnArgs
 #pragma unroll
                 for (int x = kJoinWarps / 2; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
                 M = __shfl_sync(0xffffffffu, M, 0);
-                const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                const float f = exp2f(ml.x - M);
+                const unsigned some = __ballot_sync(0xffffffffu, !paged_empty(ml.x, ml.y));
                 L = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) acc[i] = 0.f;
 #pragma unroll
                 for (int w = 0; w < kJoinWarps; ++w) {
                     const float fw = __shfl_sync(0xffffffffu, f, w);
-                    if (fw == 0.f) continue;
+                    if (!(some >> w & 1)) continue;
                     L = fmaf(fw, sh[w].y, L);
 #pragma unroll
                     for (int i = 0; i < NC; ++i) acc[i] = fmaf(fw, so[w][lane + 32 * i], acc[i]);

@@ -774,3 +774,34 @@ def test_attn_logits_of_minus_infinity(nq, n_h, d, dtype, layout):
     there = torch.where(hidden, -1, table)
     P = 2.0 ** -16 if layout == "odd" else weight_bits(nq, n_h, 2, d, dtype, False)
     check_attn(q, torch.nan_to_num(K, neginf=0.0), V, there, t, out, lse, P)
+
+
+@pytest.mark.parametrize("what", ["query", "pages", "faint"])
+@pytest.mark.parametrize("nq,n_h,d,dtype,layout", KINDS)
+def test_attn_nan_in_an_item_that_is_cut(nq, n_h, d, dtype, layout, what):
+    """A row whose logits are NaN, all of them or a long run of them, or one far below the row's largest: its out and
+    lse are NaN however its tokens are cut into pieces, and no other row changes."""
+    lens, page = [9000, 90, 9000], 16
+    max_pages = 564
+    K, V = pools(3 * max_pages + 2, page, 2, d, dtype, 11, layout)
+    table = tables(3, max_pages, 3 * max_pages + 2, 4).to(DEV)
+    t = positions(lens, nq).to(DEV)
+    q = randn((3, nq, n_h, d), 9, dtype).to(DEV)
+    bad = torch.zeros(3, nq, n_h, dtype=torch.bool, device=DEV)
+    if what == "faint":  # token 20 has nearly all of the weight
+        q[2, :, n_h // 2:] = 1.0
+        K[table[2, 1].long(), 4, 1] = 40.0
+    want, want_lse, _ = run_attn(q, K, V, table, t)
+    if what == "query":
+        q[0, nq - 1, 1] = float("nan")
+        bad[0, nq - 1, 1] = True
+    else:
+        bad[2, :, n_h // 2:] = True
+        if what == "pages":
+            K[table[2, 100:300].long(), :, 1] = float("nan")
+        else:
+            K[table[2, 400].long(), 7, 1, 3] = float("nan")
+    out, lse, _ = run_attn(q, K, V, table, t)
+    assert torch.equal(lse.isnan(), bad)
+    assert torch.equal(out.isnan(), bad[..., None].expand_as(out))
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
