@@ -63,6 +63,7 @@ struct PagedAttnArgs {
     float* lse2;
     const float* acc;
     float* acc_out;
+    bool may_have_holes() const { return n_win > 0 && nq > 1; }
 };
 
 // Tokens [0, sink) and [lo, hi) are visible to query i of sequence b, sink <= lo <= hi (empty: hi = 0).
@@ -89,8 +90,45 @@ struct PagedEntry {
     int lo_max, hi_min;
     int lo_min, hi_max, sink;
     CSA_DEV int first_token(int u, int unit) const { return (u < s1 ? u : u - s1 + w0) * unit; }
-    CSA_DEV bool seen(int j) const { return j < hi_max && (j >= lo_min || j < sink); }
 };
+
+// Queries whose windows lie apart leave holes in [lo_min, hi_max): tokens that no row of the entry sees.  There is none if
+// the queries that are not padding follow one another in steps of up to n_win, rising or falling; else there may be
+// (`apart`: begins of such a sequence, and two for a larger step).  LANES as in paged_entry.  Only kernels of calls with a
+// window and several queries (PagedAttnArgs::may_have_holes) have code for them, 2 to 5% of their time (8192 queries through
+// a window of 2048: 328 -> 334 us; 2 a sequence of 32, window 1024: 45 -> 46); in all kernels it cost the others up to 7%.
+template <int LANES>
+CSA_DEV bool paged_holes(const PagedAttnArgs& a, const PagedEntry& e)
+{
+    const int row0 = e.tile * a.R, i0 = row0 / a.G, i1 = (min(row0 + a.R, a.nq * a.G) - 1) / a.G;
+    const int64_t* ts = a.t + (int64_t)e.b * a.nq;
+    const int64_t far = (int64_t)a.cap + a.n_win;  // past it one t is as good as another
+    int apart = 0;
+#pragma unroll 1
+    for (int i = i0 + (LANES > 1 ? (int)(threadIdx.x & (LANES - 1)) : 0); i <= i1; i += LANES) {
+        const int64_t t = min(ts[i], far), before = i > i0 ? min(ts[i - 1], far) : -1;
+        if (t >= 0) apart += before < 0 ? 1 : t - before > a.n_win || before - t > a.n_win ? 2 : 0;
+    }
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) apart += __shfl_xor_sync(0xffffffffu, apart, o);
+    return apart > 1;
+}
+
+// Does some row of the entry see token j?  The K and V rows of a token that none sees may hold anything, and a weight of 0
+// does not keep a NaN out of a product: they are not read, or set to zero before.
+CSA_DEV bool paged_seen(const PagedAttnArgs& a, const PagedEntry& e, bool holes, int j)
+{
+    if (j >= e.hi_max || (j < e.lo_min && j >= e.sink)) return false;
+    if (!holes || j < e.sink) return true;
+    const int row0 = e.tile * a.R, i1 = (min(row0 + a.R, a.nq * a.G) - 1) / a.G;
+    const int64_t* ts = a.t + (int64_t)e.b * a.nq;
+#pragma unroll 1
+    for (int i = row0 / a.G; i <= i1; ++i) {
+        const int64_t t = ts[i];
+        if (j <= t && j > t - a.n_win) return true;
+    }
+    return false;
+}
 
 // LANES neighbouring lanes of a converged warp share the queries of the entry (a tile of many); 1: the
 // calling thread reads them all.  Bounds rise with t, so an entry's follow from its smallest and
@@ -126,12 +164,12 @@ CSA_DEV PagedEntry paged_entry(const PagedAttnArgs& a, int e)
         t_max = max(t_max, __shfl_xor_sync(0xffffffffu, t_max, o));
         t_seen = min(t_seen, __shfl_xor_sync(0xffffffffu, t_seen, o));
     }
-    const RowBounds first = paged_bounds_at(a, (int64_t)t_min - 1), last = paged_bounds_at(a, (int64_t)t_max - 1);
-    r.lo_max = last.lo;
-    r.hi_min = first.hi;
+    const RowBounds from = paged_bounds_at(a, (int64_t)t_min - 1), to = paged_bounds_at(a, (int64_t)t_max - 1);
+    r.lo_max = to.lo;
+    r.hi_min = from.hi;
     r.lo_min = t_max > 0 ? paged_bounds_at(a, t_seen).lo : INT32_MAX;
-    r.hi_max = last.hi;
-    r.sink = last.sink;
+    r.hi_max = to.hi;
+    r.sink = to.sink;
     r.w0 = r.hi_max > 0 ? r.lo_min / a.unit : 0;
     r.s1 = (r.sink + a.unit - 1) / a.unit;
     if (r.s1 >= r.w0) r.s1 = r.w0 = 0;  // the first tokens reach the window: one range from 0

@@ -78,8 +78,9 @@ struct Ring {
     uint32_t* masks;        // [stages]: bit r of a word: row r has a token
     const char *K, *V;      // of this key head
     int row_bytes;          // d elements
-    bool one_page;          // a unit never lies in two pages
+    bool one_page;          // a unit never lies in two pages, and has no holes
     int lane;               // within the group
+    bool holes;             // of the item
 
     // Start of the loads of unit u into `stage`; every lane of the group.
     CSA_DEV void load(const PagedAttnArgs& a, const PagedEntry& en, int u, int stage, int eb)
@@ -107,7 +108,7 @@ struct Ring {
             }
         }
         int64_t off = -1;
-        if (l < U && j0 + l < a.cap && en.seen(j0 + l)) off = paged_row(a.pl, en.b, j0 + l);
+        if (l < U && j0 + l < a.cap && paged_seen(a, en, holes, j0 + l)) off = paged_row(a.pl, en.b, j0 + l);
         const unsigned have = __ballot_sync(0xffffffffu, off >= 0);
         if (lane == 0) masks[stage] = have;
         off *= eb;
@@ -143,7 +144,7 @@ struct MmaShape {
     static constexpr int kSmem = kQ + kRing;
 };
 
-template <int DP, int WR>
+template <int DP, int WR, bool kHoles>
 __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::kCtas) paged_attn_mma(PagedAttnArgs a)
 {
     using S = MmaShape<DP, WR>;
@@ -180,6 +181,8 @@ __global__ void __launch_bounds__(MmaShape<DP, WR>::kThreads, MmaShape<DP, WR>::
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
         if (first) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
+        ring.holes = kHoles && paged_holes<1>(a, en);
+        if (kHoles) ring.one_page = a.pl.page % U == 0 && !ring.holes;
         const int n_u = sg.u1 - sg.u0;
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) {
@@ -392,7 +395,7 @@ struct FewShape {
 // lane of the 16-row kernel, whose time and power (not the cache's bytes alone) bounded long decodes: two
 // sequences of 256K tokens, width 64: 185 -> 168 us, 6.4 TB/s; 16 of up to 128K, 8 rows: 320 us, 6.6 TB/s, and at the
 // power cap 330 where the 16-row kernel took 372.
-template <int DP>
+template <int DP, bool kHoles>
 __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(PagedAttnArgs a)
 {
     using S = FewShape<DP>;
@@ -425,6 +428,8 @@ __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(Page
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
         if (first) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
+        ring.holes = kHoles && paged_holes<1>(a, en);
+        if (kHoles) ring.one_page = a.pl.page % U == 0 && !ring.holes;
         const int n_u = sg.u1 - sg.u0;
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) {
@@ -597,7 +602,7 @@ struct F32Shape {
     static constexpr int kSmem = kWarps * kStages * 2 * kU * DP * 4;
 };
 
-template <int DP, int RT>
+template <int DP, int RT, bool kHoles>
 __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(PagedAttnArgs a)
 {
     using S = F32Shape<DP, RT>;
@@ -633,6 +638,8 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
         if (sg.u0 == sg.u1) break;  // the run ends before the item's first unit
         if (lane == 0) paged_describe(a, c, sg, worker);
         const PagedEntry en = c.en;
+        ring.holes = kHoles && paged_holes<1>(a, en);
+        if (kHoles) ring.one_page = a.pl.page % U == 0 && !ring.holes;
         const int n_u = sg.u1 - sg.u0;
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) {
@@ -826,34 +833,38 @@ __global__ void __launch_bounds__(F32Shape<DP, RT>::kThreads, 1) paged_attn_f32(
 }
 
 template <auto kKernel>
+int launch_one(int threads, int smem, const PagedAttnArgs& a, cudaStream_t stream)
+{
+    if (!paged_allow_smem<kKernel>(smem)) return CSA_ERR_CUDA;
+    launch_pdl(kKernel, dim3((a.runs * a.heads + a.per_cta - 1) / a.per_cta), dim3(threads), smem, stream, a);
+    return launch_status();
+}
+template <auto kKernel, auto kWithHoles>
 int launch(int threads, int groups, int smem, PagedAttnArgs a, cudaStream_t stream)
 {
     // few workers: one or two on every SM, not eight on a few
-    const int workers = a.runs * a.heads;
-    a.per_cta = (workers + kNumSMs - 1) / kNumSMs;
+    a.per_cta = (a.runs * a.heads + kNumSMs - 1) / kNumSMs;
     if (a.per_cta > groups) a.per_cta = groups;
-    if (!paged_allow_smem<kKernel>(smem)) return CSA_ERR_CUDA;
-    launch_pdl(kKernel, dim3((workers + a.per_cta - 1) / a.per_cta), dim3(threads), smem, stream, a);
-    return launch_status();
+    return a.may_have_holes() ? launch_one<kWithHoles>(threads, smem, a, stream) : launch_one<kKernel>(threads, smem, a, stream);
 }
 
 template <int DP, int WR>
 int launch_mma(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = MmaShape<DP, WR>;
-    return launch<paged_attn_mma<DP, WR>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
+    return launch<paged_attn_mma<DP, WR, false>, paged_attn_mma<DP, WR, true>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
 template <int DP>
 int launch_few(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = FewShape<DP>;
-    return launch<paged_attn_few<DP>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
+    return launch<paged_attn_few<DP, false>, paged_attn_few<DP, true>>(S::kThreads, S::kGroups, S::kSmem, a, stream);
 }
 template <int DP, int RT>
 int launch_f32(const PagedAttnArgs& a, cudaStream_t stream)
 {
     using S = F32Shape<DP, RT>;
-    return launch<paged_attn_f32<DP, RT>>(S::kThreads, S::kWarps, S::kSmem, a, stream);
+    return launch<paged_attn_f32<DP, RT, false>, paged_attn_f32<DP, RT, true>>(S::kThreads, S::kWarps, S::kSmem, a, stream);
 }
 
 }  // namespace

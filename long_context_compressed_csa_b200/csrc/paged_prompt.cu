@@ -112,7 +112,7 @@ CSA_DEV uint32_t pages32(uint32_t have, int x)
     return (h & 1) * 0xffu | (h >> 1 & 1) * 0xff00u | (h >> 2 & 1) * 0xff0000u | (h >> 3 & 1) * 0xff000000u;
 }
 
-template <int DP, bool kOne>
+template <int DP, bool kOne, bool kHoles>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ PagedAttnArgs a, const int box_rows)
@@ -199,6 +199,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         // A row's part of a segment: loaded while the last product of the segment before runs
         struct Row {
             bool tile, in;  // the warpgroup's tile has rows; this is one
+            bool holes;     // of the item
             int64_t at;
             RowBounds rb;
         };
@@ -212,6 +213,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             const int n_rows = paged_rows(a, en.tile);
             x.tile = kOne || row0 < n_rows;
             x.in = row0 + r < n_rows;
+            x.holes = kHoles && paged_holes<32>(a, en);
             x.at = x.in ? paged_out_row(a, en.b, en.tile, h, row0 + r) : 0;
             x.rb = x.in ? paged_bounds(a, en.b, (en.tile * a.R + row0 + r) / a.G) : RowBounds{0, 0, 0};
             return x;
@@ -297,7 +299,7 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         // rows of V that no query sees: thread r has row r
                         ok = all(wait(&Vfull[vs], vt / NS));
                         if (!ok) break;
-                        if (!en.seen(j0 + r)) {
+                        if (!paged_seen(a, en, row.holes, j0 + r)) {
 #pragma unroll
                             for (int x = 0; x < DP / 8; ++x)
                                 *reinterpret_cast<uint4*>(sV + vs * S::kTile + (x >> 3) * (kT * 128) +
@@ -696,13 +698,20 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
 }
 
+template <int DP, bool kOne, bool kHoles>
+int launch_one(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box_rows, cudaStream_t stream)
+{
+    constexpr int smem = PromptShape<DP>::kSmem;
+    if (!paged_allow_smem<paged_attn_prompt<DP, kOne, kHoles>>(smem)) return CSA_ERR_CUDA;
+    launch_pdl(paged_attn_prompt<DP, kOne, kHoles>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
+    return launch_status();
+}
+
 template <int DP, bool kOne>
 int launch(const PagedAttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box_rows, cudaStream_t stream)
 {
-    constexpr int smem = PromptShape<DP>::kSmem;
-    if (!paged_allow_smem<paged_attn_prompt<DP, kOne>>(smem)) return CSA_ERR_CUDA;
-    launch_pdl(paged_attn_prompt<DP, kOne>, dim3(a.runs), dim3(kThreads), smem, stream, k, v, a, box_rows);
-    return launch_status();
+    return a.may_have_holes() ? launch_one<DP, kOne, true>(a, k, v, box_rows, stream)
+                              : launch_one<DP, kOne, false>(a, k, v, box_rows, stream);
 }
 
 }  // namespace

@@ -805,3 +805,46 @@ def test_attn_nan_in_an_item_that_is_cut(nq, n_h, d, dtype, layout, what):
     assert torch.equal(lse.isnan(), bad)
     assert torch.equal(out.isnan(), bad[..., None].expand_as(out))
     assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+
+
+def spread(nq, n_win, cap, seed):
+    """Positions whose windows leave holes: falling and far apart; in any order, with padding among them; and at the two
+    steps where a hole of one token ends: n_win + 1 and n_win."""
+    g = torch.Generator().manual_seed(seed)
+    t = torch.full((4, nq), -1, dtype=torch.int64)
+    t[0] = torch.linspace(cap - 1, 5, nq).long() if nq > 1 else cap - 1
+    t[1] = torch.randint(-cap // 4, cap, (nq,), generator=g).clamp(min=-1)
+    at = 7
+    for i in range(nq):
+        t[2, i] = min(at, cap - 1)
+        at += n_win + 1 if i % 3 == 1 else n_win if i % 3 == 0 else 1
+    t[3, 0], t[3, nq - 1], t[3, nq // 2] = 30, cap + 3, 30 + n_win // 2
+    return t
+
+
+@pytest.mark.parametrize("n_win,n_sink", [(1, 0), (16, 3), (50, 70)])
+@pytest.mark.parametrize("nq,n_h,d,dtype,layout", [
+    (2, 4, 64, torch.bfloat16, "nhd"), (4, 4, 256, torch.bfloat16, "hnd"), (8, 4, 128, torch.bfloat16, "nhd"),
+    (15, 4, 64, torch.bfloat16, "nhd"), (33, 2, 256, torch.bfloat16, "nhd"), (50, 4, 128, torch.bfloat16, "nhd"),
+    (50, 2, 64, torch.bfloat16, "hnd"), (150, 4, 128, torch.bfloat16, "nhd"), (3, 2, 64, torch.float32, "nhd"),
+    (20, 4, 128, torch.float32, "hnd"), (9, 2, 256, torch.float32, "nhd"), (7, 4, 40, torch.bfloat16, "odd")])
+@pytest.mark.parametrize("page", [16, 24])
+def test_attn_rows_between_windows_reach_nothing(nq, n_h, d, dtype, layout, n_win, n_sink, page):
+    cap = page * (912 // page)
+    B, max_pages = 4, cap // page
+    n_pages = B * max_pages + 1
+    K, V = pools(n_pages, page, 2, d, dtype, 21, layout)
+    table = tables(B, max_pages, n_pages, 6)
+    t = spread(nq, n_win, cap, nq)
+    j = torch.arange(cap)
+    seen = ((j <= t[..., None]) & ((j > t[..., None] - n_win) | (j < n_sink))).any(1)  # [B, cap]
+    used = torch.zeros(n_pages, page, dtype=torch.bool)
+    for b in range(B):
+        used[table[b].long()[j // page], j % page] = seen[b]
+    K[~used.to(DEV)], V[~used.to(DEV)] = float("nan"), float("nan")
+    table, t = table.to(DEV), t.to(DEV)
+    q = randn((B, nq, n_h, d), 9, dtype, scale=2.0).to(DEV)
+    acc = torch.rand(B, 2, cap, device=DEV)
+    out, lse, acc_out = run_attn(q, K, V, table, t, n_win, n_sink, acc=acc)
+    P = 2.0 ** -16 if layout == "odd" else weight_bits(nq, n_h, 2, d, dtype, True)
+    check_attn(q, torch.nan_to_num(K), torch.nan_to_num(V), table, t, out, lse, P, n_win, n_sink, acc=acc, acc_out=acc_out)
