@@ -471,6 +471,13 @@ int csa_workspace_status(const void* workspace, csa_stream_t stream);
  * idx_out is invalid.  workspace: 16-byte aligned; cycles >= 0 (CSA_ERR_ARG otherwise). */
 int csa_workspace_set_wait_budget(void* workspace, int64_t cycles, csa_stream_t stream);
 
+/* The same test hook for paged_attn, whose workspace has no set contents: the budget in SM clock cycles of the waits of its
+ * tensor-core prompt kernel (33 packed rows or more) in this process's later calls.  cycles = 0: a wait that is not over at
+ * its first look gives up; cycles < 0 restores the ~1 s budget.  A captured call keeps the budget of its capture.  After a
+ * timeout each CTA waits, by the ~1 s budget, for its own copies and products and ends; the call's outputs are then invalid
+ * and csa_workspace_status says so. */
+int paged_attn_set_wait_budget(int64_t cycles);
+
 /* Zero `bytes` of device memory on `stream` (cudaMemsetAsync); for first-use workspaces. */
 int csa_workspace_zero(void* workspace, size_t bytes, csa_stream_t stream);
 

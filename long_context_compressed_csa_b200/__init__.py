@@ -34,6 +34,7 @@ from ._binding import (  # noqa: F401
     library_path,
     paged_append,
     paged_attn,
+    paged_attn_set_wait_budget,
     paged_attn_workspace_size,
     paged_evict,
 )

@@ -52,6 +52,7 @@ _SIGS = {
     "paged_attn_workspace_size": ([i32, i32, i32, i32, i32, i64, i32], sz),
     "paged_attn": ([vp, vp, vp, i64, i64, i64, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp,
                     vp, vp, vp, sz, i32, i32, vp], i32),
+    "paged_attn_set_wait_budget": ([i64], i32),
     "paged_evict": ([vp, vp, i64, i64, i64, i64, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp,
                      vp, i32, vp], i32),
 }
@@ -431,6 +432,12 @@ def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
 def paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, weights=False) -> int:
     """Bytes of workspace of paged_attn; cap = max_pages * page, weights: with acc."""
     return int(library().paged_attn_workspace_size(*_i32(B, nq, n_h, n_kv, d), int(cap), 1 if weights else 0))
+
+
+def paged_attn_set_wait_budget(cycles):
+    """Test hook: the wait budget (SM cycles) of paged_attn's prompt kernel in later calls of the process; < 0 restores
+    the default."""
+    _check("paged_attn_set_wait_budget", library().paged_attn_set_wait_budget(int(cycles)))
 
 
 def paged_attn(q, K_pages, V_pages, table, t, out, workspace, lse=None, scale=0.0, n_win=0, n_sink=0, acc=None,

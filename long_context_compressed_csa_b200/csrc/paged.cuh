@@ -51,6 +51,7 @@ struct PagedAttnArgs {
     int heads;             // lists of runs: worker w has run w / heads (prompt and CUDA-core kernels: one list, a worker
                            // is a CTA; decode kernels: a list for each key head, a worker is a group of warps)
     int per_cta;           // decode kernels: workers of a CTA
+    long long wait_budget; // clocks, of the prompt kernel's waits
     // workspace
     uint32_t* status;      // 1 after a timeout
     int4* desc;            // [workers]: the split item that begins in this worker's run {entry, head, runs that have a

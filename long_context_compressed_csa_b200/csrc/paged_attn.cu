@@ -362,6 +362,9 @@ static int64_t paged_places(const PagedShape& s, int B, int nq, int G, int n_kv,
     return (std::max<int64_t>(1, (cap + s.unit - 1) / s.unit) + s.item_units) * B * tiles * (s.by_head ? 1 : n_kv);
 }
 
+// A budget that the test hook set; negative: the one of every other device wait.
+static std::atomic<int64_t> g_wait_budget{-1};
+
 // Workspace layout, from the sizes alone: room for every kernel that a call of these sizes may run on.
 struct PagedPlan {
     size_t part_o, part_ml, logits, lse2, bytes;  // offsets; before them the 256-byte status block and desc
@@ -403,6 +406,12 @@ extern "C" size_t paged_attn_workspace_size(int B, int nq, int n_h, int n_kv, in
         cap > INT32_MAX || (int64_t)nq * n_h > INT32_MAX / 2 || (int64_t)B * nq > INT32_MAX / 2)
         return 0;
     return paged_plan(B, nq, n_h / n_kv, n_kv, d, cap, weights != 0).bytes;
+}
+
+extern "C" int paged_attn_set_wait_budget(int64_t cycles)
+{
+    csa::g_wait_budget.store(cycles, std::memory_order_relaxed);
+    return CSA_OK;
 }
 
 extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t pool_ld_page, int64_t pool_ld_row,
@@ -447,6 +456,8 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     a.n_tiles = (nq * G + sp.R - 1) / sp.R;
     a.heads = sp.by_head ? n_kv : 1;
     a.runs = paged_runs(sp, a.heads, paged_places(sp, B, nq, G, n_kv, cap));
+    const int64_t budget = g_wait_budget.load(std::memory_order_relaxed);
+    a.wait_budget = budget < 0 ? tc::kWaitBudget : budget;
     char* ws = static_cast<char*>(workspace);
     a.status = reinterpret_cast<uint32_t*>(ws);
     a.desc = reinterpret_cast<int4*>(ws + 256);

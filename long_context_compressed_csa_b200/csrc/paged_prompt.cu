@@ -172,17 +172,19 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     PagedCursor c;
     const bool some = paged_schedule<kThreads, 8, false>(a, cta, sh, c);
     // false after a timeout; the caller leaves its loops
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
+    auto wait_for = [&](uint64_t* bar, uint32_t phase, long long budget) {
         // no sleep between the polls: a wake-up costs more than the waits of this kernel last
-        if (tc::mbar_try_wait(bar, phase & 1)) return true;
+        if (tc::mbar_test(bar, phase & 1)) return true;
         const long long t0 = clock64();
-        while (!tc::mbar_try_wait(bar, phase & 1))
-            if (clock64() - t0 > tc::kWaitBudget) {
+        do {
+            if (clock64() - t0 > budget) {
                 failed = 1;
                 return false;
             }
+        } while (!tc::mbar_try_wait(bar, phase & 1));
         return true;
     };
+    auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_for(bar, phase, a.wait_budget); };
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };  // a warp gives up as one
 
     if (some && warp < 8) {
@@ -549,9 +551,9 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 }
                 if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
-            // no copy is in flight when the CTA ends: on the normal path the products have waited for them
-            if (!ok)
-                for (uint32_t k = n >= NS ? n - NS : 0; k < n; ++k) wait(&fulls[k % NS], k / NS);
+            // No copy is in flight when the CTA ends, whichever warp gave up: on the normal path the products wait for them,
+            // but after a timeout elsewhere they may not have.
+            for (uint32_t k = n >= NS ? n - NS : 0; k < n; ++k) wait_for(&fulls[k % NS], k / NS, tc::kWaitBudget);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ products
             constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kM, kT, false, false);
@@ -681,11 +683,10 @@ paged_attn_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 }
                 if (!ok || !paged_next<32, false>(a, c, sg)) break;
             }
-            if (!ok) {  // nor a product: they read shared memory and write TMEM
-                if (elect()) tc::mma_commit(&drained);
-                __syncwarp();
-                wait(&drained, 0);
-            }
+            // nor a product: they read shared memory and write TMEM
+            if (elect()) tc::mma_commit(&drained);
+            __syncwarp();
+            wait_for(&drained, 0, tc::kWaitBudget);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -848,3 +848,32 @@ def test_attn_rows_between_windows_reach_nothing(nq, n_h, d, dtype, layout, n_wi
     out, lse, acc_out = run_attn(q, K, V, table, t, n_win, n_sink, acc=acc)
     P = 2.0 ** -16 if layout == "odd" else weight_bits(nq, n_h, 2, d, dtype, True)
     check_attn(q, torch.nan_to_num(K), torch.nan_to_num(V), table, t, out, lse, P, n_win, n_sink, acc=acc, acc_out=acc_out)
+
+
+# ==================================================================================
+# waits that run out
+# ==================================================================================
+@pytest.mark.parametrize("budget", [0, 100, 500, 2000, 8000])
+@pytest.mark.parametrize("nq,d,n_win", [(40, 128, 0), (33, 64, 50), (150, 128, 0), (300, 64, 70)])
+def test_prompt_waits_that_run_out_are_reported(nq, d, n_win, budget):
+    """Failure detection without a GPU fault: with a budget of a few clocks the prompt kernel's bounded waits run out,
+    wherever its warps happen to be; the call says so through the workspace's status, and the next call is right."""
+    K, V = pools(140, 16, 2, d, torch.bfloat16, 5)
+    table = tables(2, 66, 140, 1).to(DEV)
+    q = randn((2, nq, 8, d), 9).to(DEV)
+    t = positions([1050, 400], nq).to(DEV)
+    ws = torch.empty(lib.paged_attn_workspace_size(2, nq, 8, 2, d, 1056, True), dtype=torch.uint8, device=DEV)
+    acc = torch.zeros(2, 2, 1056, device=DEV)
+    want = run_attn(q, K, V, table, t, n_win, 4, acc=acc, ws=ws)
+    assert lib.csa_workspace_status(ws) == 0
+    try:
+        lib.paged_attn_set_wait_budget(budget)
+        got = run_attn(q, K, V, table, t, n_win, 4, acc=acc, ws=ws)
+    finally:
+        lib.paged_attn_set_wait_budget(-1)
+    status = lib.csa_workspace_status(ws)
+    assert status in ((-7,) if budget == 0 else (0, -7))
+    again = run_attn(q, K, V, table, t, n_win, 4, acc=acc, ws=ws)
+    assert lib.csa_workspace_status(ws) == 0
+    for x, y, z in zip(want, got, again):
+        assert torch.equal(x, z) and (status != 0 or torch.equal(x, y))
