@@ -385,7 +385,8 @@ int hca_dense_attn_window(const void* q, const void* cache, const int64_t* t, co
  * table  : int32 [B, max_pages] (device).  Token j of sequence b, 0 <= j < cap =
  *          max_pages * page, lies in page table[b][j / page], row j mod page.  An entry
  *          outside [0, n_pages) means that there is no page: its tokens are never read
- *          or written, and no query sees them.  Sequences may share pages that no call writes.
+ *          or written, and no query sees them.  With max_pages = 0 the table and the pools may be null
+ *          (paged_append, paged_attn).  Sequences may share pages that no call writes.
  * t      : int64 [B, nq] (device): the cache position of each new token; t < 0 marks
  *          padding.  Positions count cached tokens, so after paged_evict they go on
  *          from the new length.

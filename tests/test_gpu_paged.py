@@ -877,3 +877,18 @@ def test_prompt_waits_that_run_out_are_reported(nq, d, n_win, budget):
     assert lib.csa_workspace_status(ws) == 0
     for x, y, z in zip(want, got, again):
         assert torch.equal(x, z) and (status != 0 or torch.equal(x, y))
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_no_capacity_needs_no_pools(nq):
+    """The C call with max_pages = 0: the pools and the table may be null, and every query sees nothing."""
+    import ctypes
+    q = randn((2, nq, 8, 128), 9).to(DEV)
+    out, lse = torch.full_like(q, 7.0), torch.full((2, nq, 8), 7.0, device=DEV)
+    t = positions([60, 45], nq).to(DEV)
+    ws = torch.empty(lib.paged_attn_workspace_size(2, nq, 8, 2, 128, 0), dtype=torch.uint8, device=DEV)
+    p = lambda x: ctypes.c_void_p(x.data_ptr())  # noqa: E731
+    assert lib.library().paged_attn(p(q), None, None, 16 * 256, 256, 128, 4, 16, None, 0, p(t), 2, nq, 8, 2, 128, 0, 0, 0.0,
+                                    p(out), p(lse), None, None, p(ws), ws.nbytes, 0, 1,
+                                    ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
