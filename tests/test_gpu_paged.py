@@ -892,3 +892,53 @@ def test_no_capacity_needs_no_pools(nq):
                                     p(out), p(lse), None, None, p(ws), ws.nbytes, 0, 1,
                                     ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+# ==================================================================================
+# accumulated weights of every kernel, and in captured calls
+# ==================================================================================
+@pytest.mark.parametrize("n_win,n_sink", [(0, 0), (40, 5)])
+@pytest.mark.parametrize("nq,n_h,n_kv,d,page", [
+    (1, 8, 2, 256, 16), (2, 6, 2, 256, 16),         # 8 rows or fewer of wide heads: two warps a worker
+    (3, 16, 2, 128, 16), (2, 24, 2, 64, 32),        # 17 to 32 rows
+    (4, 16, 2, 256, 16), (5, 24, 2, 256, 16),       # ... of wide heads, and 60
+    (5, 32, 2, 128, 16), (40, 2, 2, 64, 64), (5, 16, 1, 96, 8),  # one tile of the prompt kernel
+    (60, 8, 2, 128, 16), (140, 4, 2, 64, 32),       # two tiles, and a third
+    (1, 8, 2, 64, 3), (50, 4, 2, 64, 7)])           # a capacity that is no multiple of 4
+def test_weights_of_every_kernel(nq, n_h, n_kv, d, page, n_win, n_sink):
+    case([nq, 300, 2999], nq=nq, n_h=n_h, n_kv=n_kv, d=d, page=page, n_win=n_win, n_sink=n_sink, acc=True, seed=nq)
+
+
+@pytest.mark.parametrize("nq,n_h", [(1, 8), (3, 16), (40, 8)])
+def test_graphs_accumulate_the_weights_of_their_lengths(nq, n_h):
+    """Two captured graphs share a workspace; in each a call that accumulates and one that does not. Every replay's
+    increment, outputs and log-sum-exps are those of the lengths that it finds."""
+    K, V = pools(70, 16, 2, 128, torch.bfloat16, 5)
+    table = tables(2, 30, 70, 1).to(DEV)
+    qs = [randn((2, nq, n_h, 128), 9 + i).to(DEV) for i in range(2)]
+    ts = [positions([100, 70], nq).to(DEV) for _ in qs]
+    outs = [[torch.empty_like(q) for _ in range(2)] for q in qs]
+    lses = [[torch.empty(2, nq, n_h, device=DEV) for _ in range(2)] for _ in qs]
+    accs = [torch.rand(2, 2, 480, device=DEV) for _ in qs]
+    ws = torch.empty(lib.paged_attn_workspace_size(2, nq, n_h, 2, 128, 480, True), dtype=torch.uint8, device=DEV)
+    lib.paged_attn(qs[0], K, V, table, ts[0], outs[0][0], ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for x in range(2):
+                lib.paged_attn(qs[i], K, V, table, ts[i], outs[i][x], ws, lse=lses[i][x], n_win=64 * i, n_sink=4,
+                               acc=None if x else accs[i])
+        graphs.append(g)
+    P = weight_bits(nq, n_h, 2, 128, torch.bfloat16, True)
+    for lens in ([100, 70], [480, nq], [max(nq, 33), 470], [nq, 2 * nq]):
+        before = [a.clone() for a in accs]
+        for i in range(2):
+            ts[i].copy_(positions(lens, nq))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for x in range(2):
+                check_attn(qs[i], K, V, table, ts[i], outs[i][x], lses[i][x], P, 64 * i, 4, acc=None if x else before[i],
+                           acc_out=None if x else accs[i])
