@@ -430,7 +430,8 @@ def paged_append(k, v, K_pages, V_pages, table, t, stream=None):
 
 
 def paged_attn_workspace_size(B, nq, n_h, n_kv, d, cap, weights=False) -> int:
-    """Bytes of workspace of paged_attn; cap = max_pages * page, weights: with acc."""
+    """Bytes of workspace of paged_attn; cap = max_pages * page, weights: with acc (the logits, 4 B nq n_h cap bytes, are
+    in it then)."""
     return int(library().paged_attn_workspace_size(*_i32(B, nq, n_h, n_kv, d), int(cap), 1 if weights else 0))
 
 

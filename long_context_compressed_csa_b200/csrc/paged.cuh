@@ -374,6 +374,12 @@ CSA_DEV int64_t paged_out_row(const PagedAttnArgs& a, int b, int tile, int h, in
     return ((int64_t)b * a.nq + i) * a.n_h + h * a.G + (row - i * a.G);
 }
 
+CSA_DEV uint32_t pack2(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Stores of one result: element `at` of out, and a row's log-sum-exp (natural for the caller,
 // base 2 for the accumulated weights) from its running maximum and sum.
 CSA_DEV void paged_store(const PagedAttnArgs& a, int64_t at, float v)

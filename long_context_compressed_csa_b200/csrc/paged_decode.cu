@@ -47,11 +47,6 @@ CSA_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-CSA_DEV uint32_t pack2(float x, float y)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 CSA_DEV float lo16(uint32_t u) { return __uint_as_float(u << 16); }
 CSA_DEV float hi16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -393,8 +388,8 @@ struct FewShape {
 // A lane has two rows (2 (lane mod 4) and the next) and tokens, or columns, lane / 4 and 8 more.  P^T becomes the
 // second product's operand by a transposition of its 8 x 8 blocks.  Half the tensor work and half the logits a
 // lane of the 16-row kernel, whose time and power (not the cache's bytes alone) bounded long decodes: two
-// sequences of 256K tokens, width 64: 185 -> 168 us, 6.4 TB/s; 16 of up to 128K, 8 rows: 320 us, 6.6 TB/s, and at the
-// power cap 330 where the 16-row kernel took 372.
+// sequences of 256K tokens, width 64: 185 us, now 166 to 177 (6.1 to 6.5 TB/s); 16 of up to 128K, 8 rows: 322 to 330 us,
+// 6.5 to 6.7 TB/s, at the power cap too, where the 16-row kernel took 372.
 template <int DP, bool kHoles>
 __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(PagedAttnArgs a)
 {
@@ -589,8 +584,8 @@ __global__ void __launch_bounds__(FewShape<DP>::kThreads, 1) paged_attn_few(Page
 }
 
 // fp32 rows: RT of them in registers, EL = 64 / RT elements of a row a lane, so that q and the output take 128
-// registers for either RT.  Bound by FMA and shuffle issue at 8 rows (16 sequences of up to 8K tokens, 545 MB: 126 us,
-// 4.3 TB/s), by latency in small calls (8 of up to 4K, 69 MB: 26 us).
+// registers for either RT.  Bound by FMA and shuffle issue at 8 rows (16 sequences of 8K tokens, 537 MB: 128 us, 4.2 TB/s;
+// 4 rows: 105 us, 5.1 TB/s), by latency in small calls (8 of up to 4K, 69 MB: 30 us).
 template <int DP, int RT>
 struct F32Shape {
     static constexpr int kEL = 64 / RT;      // elements of a row that a lane has

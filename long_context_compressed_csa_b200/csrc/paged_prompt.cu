@@ -25,8 +25,9 @@
 // The masks (positions, window, first tokens, missing pages) are applied to S only in units that
 // are not wholly visible; there the rows of V that no query sees are set to zero too, since 0 x NaN
 // would reach the sums.  Bounded waits: a timeout ends the CTA and sets its status.
-// 2 x 1024 queries over 15-16K tokens, 64 / 8 heads, d = 128: 923 us, 1104 TFLOP/s, 0.68 of the measured GEMM (1050 to
-// 1109 us at the power cap).  A unit of both tiles takes 3500 clocks, 2048 of which are products: a tile's
+// 2 x 1024 queries over 15-16K tokens, 64 / 8 heads, d = 128: 1010 to 1100 us by the power cap (926 to 1008 TFLOP/s, 0.68 to
+// 0.74 of the sustained GEMM); 1 x 1024 over 8K, 32 heads, d = 128: 154 us, below the cap.  d = 64, 2 x 1024 over 8K, 32 / 8
+// heads: 214 us, 0.60 PFLOP/s.  A unit of both tiles takes 3500 clocks, 2048 of which are products: a tile's
 // softmax (2100) and its products (1100 with their barriers) take turns, and there is no TMEM for a second S.
 #include "paged.cuh"
 #include "tc_utils.cuh"
@@ -79,11 +80,6 @@ CSA_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x
         "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(tc::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(h), "r"(r), "r"(p)
         : "memory");
-}
-CSA_DEV uint32_t pack2(float x, float y)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // One lane of a converged warp.
