@@ -451,7 +451,8 @@ extern "C" int paged_attn(const void* q, const void* K, const void* V, int64_t p
     // 16-byte loads and stores: every row starts on a 16-byte boundary and is whole 16-byte words
     const int64_t lds = pool_ld_page | pool_ld_row | (n_kv > 1 ? pool_ld_head : 0) | d;
     // (without a capacity the pools may be null: the CUDA-core kernel forms no address from them)
-    const bool wide = cap > 0 && aligned16(q) && aligned16(K) && aligned16(V) && aligned16(out) && lds * elem_bytes(dtype) % 16 == 0;
+    const bool wide = cap > 0 && aligned16(q) && aligned16(K) && aligned16(V) && aligned16(out) &&
+                      lds * elem_bytes(dtype) % 16 == 0;
     const PagedShape sp = paged_shape(dtype, wide, paged_prompt_takes(pl, n_kv, d), nq * G, d);
     a.R = sp.R; a.unit = sp.unit; a.min_units = sp.min_units; a.item_units = sp.item_units;
     a.n_tiles = (nq * G + sp.R - 1) / sp.R;

@@ -88,8 +88,8 @@ CSA_DEV int2 remote2(const int* p, uint32_t rank, bool far)
 // histograms took 10,000 clocks a pass with 8 CTAs).  Then each warp counts what stays of its own
 // neighbouring tokens, and a prefix sum over the CTA and the CTAs before it gives their places in the output.
 // Keys stay in registers when a run is no longer than T * kKeys, else each pass reads them again.
-// Bound by latency, a chain of reads, shared-memory atomics and eleven cluster barriers (three a pass, two about the counts): 8 heads of 128K tokens take 45 us
-// (384 with one CTA a head), 16 sequences of 8K about 27.
+// Bound by latency, a chain of reads, shared-memory atomics and eleven cluster barriers (three a pass, two about the
+// counts): 8 heads of 128K tokens take 45 us (384 with one CTA a head), 16 sequences of 8K about 27.
 template <int T>
 __global__ void __launch_bounds__(T, 1024 / T) paged_evict_select(EvictArgs a)
 {

@@ -942,3 +942,78 @@ def test_graphs_accumulate_the_weights_of_their_lengths(nq, n_h):
             for x in range(2):
                 check_attn(qs[i], K, V, table, ts[i], outs[i][x], lses[i][x], P, 64 * i, 4, acc=None if x else before[i],
                            acc_out=None if x else accs[i])
+
+
+# ==================================================================================
+# captured serving steps, and calls with nothing to do
+# ==================================================================================
+def test_a_captured_step_appends_attends_and_evicts():
+    """One graph: append, attention that accumulates, eviction to other pages. Every replay is right for the tokens,
+    positions and lengths that it finds, and leaves the old pages as they were."""
+    B, n_h, n_kv, d, page, max_pages, keep = 3, 8, 2, 64, 16, 20, 64
+    n_pages = B * (max_pages + 4)
+    K, V = pools(n_pages, page, n_kv, d, torch.bfloat16, 31)
+    both = tables(B, max_pages + 4, n_pages, 2).to(DEV)
+    table, new_table = both[:, :max_pages].contiguous(), both[:, max_pages:].contiguous()
+    cap = max_pages * page
+    k, v = (torch.empty(B, 1, n_kv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q = torch.empty(B, 1, n_h, d, dtype=torch.bfloat16, device=DEV)
+    t, lens = torch.zeros(B, 1, dtype=torch.int64, device=DEV), torch.ones(B, dtype=torch.int64, device=DEV)
+    acc, out, lse = torch.zeros(B, n_kv, cap, device=DEV), torch.empty_like(q), torch.empty(B, 1, n_h, device=DEV)
+    new_lens, idx = torch.zeros_like(lens), torch.zeros(B, n_kv, keep, dtype=torch.int32, device=DEV)
+    new_acc = torch.zeros(B, n_kv, 4 * page, device=DEV)
+    ws = torch.empty(lib.paged_attn_workspace_size(B, 1, n_h, n_kv, d, cap, True), dtype=torch.uint8, device=DEV)
+
+    def step():
+        lib.paged_append(k, v, K, V, table, t)
+        lib.paged_attn(q, K, V, table, t, out, ws, lse=lse, acc=acc)
+        lib.paged_evict(K, V, table, lens, acc, keep, new_table, new_lens, new_acc, idx, n_sink=2, n_recent=8)
+
+    for x in (k, v, q):
+        x.zero_()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i, ns in enumerate(([300, 65, 1], [64, 320, 200], [301, 66, 2])):
+        for j, x in enumerate((k, v, q)):
+            x.copy_(randn(tuple(x.shape), 50 + 3 * i + j))
+        lens.copy_(torch.tensor(ns))
+        t.copy_(positions(ns, 1))
+        acc.copy_(torch.rand(B, n_kv, cap))
+        before, wk, wv = acc.clone(), to_f64(K), to_f64(V)
+        graph.replay()
+        torch.cuda.synchronize()
+        O.append(to_f64(k), to_f64(v), wk, wv, table.cpu().numpy(), t.cpu().numpy())
+        check_attn(q, torch.tensor(wk), torch.tensor(wv), table, t, out, lse, 2.0 ** -16, acc=before, acc_out=acc)
+        want = O.evict(wk, wv, table.cpu().numpy(), np.array(ns), acc.cpu().numpy(), keep, new_table.cpu().numpy(), 2, 8)
+        np.testing.assert_array_equal(new_lens.cpu().numpy(), want[0])
+        np.testing.assert_array_equal(new_acc.cpu().numpy(), want[1])
+        np.testing.assert_array_equal(idx.cpu().numpy(), want[2])
+        np.testing.assert_array_equal(to_f64(K), wk)
+        np.testing.assert_array_equal(to_f64(V), wv)
+
+
+def test_calls_with_nothing_to_do():
+    K, V = pools(6, 16, 2, 64, torch.bfloat16, 5)
+    wk, wv = K.clone(), V.clone()
+    i32, i64 = dict(dtype=torch.int32, device=DEV), dict(dtype=torch.int64, device=DEV)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    for B, nq in ((0, 1), (2, 0)):  # no sequences, no queries
+        x = torch.empty(B, nq, 2, 64, dtype=torch.bfloat16, device=DEV)
+        table, t = torch.zeros(B, 2, **i32), torch.zeros(B, nq, **i64)
+        lib.paged_append(x, x, K, V, table, t)
+        lib.paged_attn(x, K, V, table, t, torch.empty_like(x), ws)
+    none = torch.zeros(0, 2, **i32)
+    lib.paged_evict(K, V, none, torch.zeros(0, **i64), torch.zeros(0, 2, 32, device=DEV), 4, none[:, :1].contiguous(),
+                    torch.zeros(0, **i64), torch.zeros(0, 2, 16, device=DEV), torch.zeros(0, 2, 4, **i32))
+    # a cache without pages: nothing is kept, whatever its lengths say
+    new = torch.tensor([[3], [4]], **i32)
+    idx, new_lens, new_acc = run_evict(K, V, torch.zeros(2, 0, **i32), torch.tensor([5, 0], **i64),
+                                       torch.zeros(2, 2, 0, device=DEV), 4, new)
+    assert new_lens.tolist() == [0, 0] and bool((idx == -1).all()) and bool((new_acc == 0).all())
+    ones = torch.ones(2, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    lib.paged_append(ones, ones, K, V, torch.zeros(2, 0, **i32), torch.zeros(2, 1, **i64))
+    torch.cuda.synchronize()
+    assert torch.equal(K, wk) and torch.equal(V, wv)
